@@ -28,6 +28,16 @@
  *   ssm_conv_state_update  the same step with the depthwise causal-conv1d
  *                     step of Mamba.step() in front of it (roll conv_state
  *                     left, append x, sum conv_state * weight + bias, SiLU).
+ *   ssm_gated_scan_fwd / _bwd, ssm_gated_state_update  a gated linear
+ *                     recurrence: one state per channel whose decay and input
+ *                     factor come from per-step gates.
+ *   ssm_conv1d_fwd / _bwd / _update  the causal depthwise convolution of the
+ *                     block over a whole sequence, its gradients, and its
+ *                     one-token step by itself.
+ *   ssm_gated_norm_fwd / _bwd  RMS norm by groups with the SiLU gate, in front
+ *                     of the block's output projection.
+ *   ssm_add_norm_fwd / _bwd  the block's output normed, scaled and added to
+ *                     the residual, and the next block's RMS norm of the sum.
  *
  * Conventions for every entry point:
  *   - Pointers marked "device" point to device memory of the current CUDA
@@ -471,6 +481,234 @@ ssm_status ss2d_cross_merge_ex(const void *ys, void *y, int64_t b, int64_t H,
 ssm_status ss2d_cross_merge(const void *ys, void *y, int64_t b, int64_t H,
                             int64_t W, int64_t d_in, ssm_dtype dtype,
                             ssm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Around the scan: the gated recurrence, the causal convolution over a
+ * sequence, and the norms of a block.
+ *
+ * Rows with a stride: every activation of these calls has its own row stride
+ * NAME_ld, in elements: row r (of b * L, of b, or of `rows`) starts at
+ * NAME + r * NAME_ld, its channels are adjacent, and NAME_ld >= channels.  So
+ * x and z may be the two halves of one projection's rows, and their gradients
+ * the two halves of one buffer.  Rows of outputs may interleave with rows of
+ * other arguments of the same stride, but share no element with them.  States,
+ * windows, parameters and their gradients are contiguous.
+ *
+ * seq_start: device uint8 (b, L), nullable.  Where it is not 0 a new sequence
+ * begins at that step (packed documents): nothing from the steps before it,
+ * the start state or the window reaches it or a later step, infinities and
+ * NaN included, and no gradient goes back across it.
+ *
+ * Gradients of parameters are summed over rows in a fixed order (partial sums
+ * in the workspace, then one sum over them): the same call gives the same
+ * bits again on the same device.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Gated linear recurrence over a sequence.  For every batch i and channel d,
+ * with h starting at h0[i,d] (or 0) and for t = 0 .. L-1:
+ *     r = sigmoid(gate_a[i,t,d] + bias_a[d]),  g = sigmoid(gate_x[i,t,d] + bias_x[d])
+ *     a = exp(A[d] * r)
+ *     h = a * h + sqrt(1 - a^2) * g * u[i,t,d]      (h = g * u where a sequence starts)
+ *     y[i,t,d] = z ? h * silu(z[i,t,d]) : h
+ * and h_last[i,d] = h after the last step.  A holds log decays: values <= 0
+ * (above 0 the decay exceeds 1 and the input factor is 0).
+ *
+ *   u, gate_a, gate_x, z, y   device rows (b L, d_in), dtype; z nullable
+ *   A                         device fp32 (d_in)
+ *   bias_a, bias_x            device fp32 (d_in), nullable (0)
+ *   h0, h_last                device fp32 (b, d_in), nullable; h_last may equal h0
+ *   chunk_states              device fp32, nullable: the state in front of every
+ *                             64th step, (b, ceil(L / 64), d_in), for
+ *                             ssm_gated_scan_bwd; chunk_states_bytes >=
+ *                             ssm_gated_scan_states_bytes(b, L, d_in)
+ * Arithmetic and state are fp32; y is rounded once.
+ */
+ssm_status ssm_gated_scan_fwd(const void *u, int64_t u_ld, const void *gate_a, int64_t gate_a_ld,
+                              const void *gate_x, int64_t gate_x_ld, const float *A,
+                              const float *bias_a, const float *bias_x, const void *z,
+                              int64_t z_ld, const uint8_t *seq_start, const float *h0,
+                              float *h_last, void *y, int64_t y_ld, float *chunk_states,
+                              size_t chunk_states_bytes, int64_t b, int64_t L, int64_t d_in,
+                              ssm_dtype dtype, ssm_stream_t stream);
+
+/* Bytes of chunk_states: b * ceil(L / 64) * d_in * 4; (size_t)-1 for invalid sizes. */
+size_t ssm_gated_scan_states_bytes(int64_t b, int64_t L, int64_t d_in);
+
+/*
+ * Gradients of sum dout * y + sum dh_last * h_last for ssm_gated_scan_fwd with
+ * the same inputs, from the chunk_states it wrote.  With lam = d loss / d h_t
+ * (lam_t = dout_t silu(z_t) + a_{t+1} lam_{t+1}, f = sqrt(1 - a^2)):
+ *     du = lam f g;  dgate_x = lam f u g (1 - g);  dz = dout h silu'(z)
+ *     dl = lam (a h_{t-1} - a^2 g u / f)   (0 where a sequence starts, and its
+ *                                           second term 0 where f = 0)
+ *     dA = sum dl r;  dgate_a = dl A r (1 - r);  dh0 = a_0 lam_0
+ * dbias_a, dbias_x are the sums of dgate_a, dgate_x over b and L.
+ *
+ *   dout                       device rows (b L, d_in), dtype
+ *   dh_last                    device fp32 (b, d_in), nullable (0)
+ *   du, dgate_a, dgate_x, dz   device rows (b L, d_in), dtype; dz is required
+ *                              with z and not written without
+ *   dA, dbias_a, dbias_x       device fp32 (d_in); the two biases nullable
+ *   dh0                        device fp32 (b, d_in), nullable; may equal dh_last
+ *   workspace                  device, 16-byte aligned, >=
+ *                              ssm_gated_scan_bwd_workspace_bytes(...) bytes;
+ *                              contents on entry are not read
+ */
+ssm_status ssm_gated_scan_bwd(const void *u, int64_t u_ld, const void *gate_a, int64_t gate_a_ld,
+                              const void *gate_x, int64_t gate_x_ld, const float *A,
+                              const float *bias_a, const float *bias_x, const void *z,
+                              int64_t z_ld, const uint8_t *seq_start, const void *dout,
+                              int64_t dout_ld, const float *dh_last, void *du, int64_t du_ld,
+                              void *dgate_a, int64_t dgate_a_ld, void *dgate_x,
+                              int64_t dgate_x_ld, void *dz, int64_t dz_ld, float *dA,
+                              float *dbias_a, float *dbias_x, float *dh0, int64_t b, int64_t L,
+                              int64_t d_in, ssm_dtype dtype, const float *chunk_states,
+                              size_t chunk_states_bytes, void *workspace, size_t workspace_bytes,
+                              ssm_stream_t stream);
+
+/* Bytes of ssm_gated_scan_bwd's workspace on the current device; (size_t)-1 for
+ * invalid sizes. */
+size_t ssm_gated_scan_bwd_workspace_bytes(int64_t b, int64_t L, int64_t d_in);
+
+/*
+ * One token of the recurrence above, in place on state (b, d_in) fp32; u,
+ * gate_a, gate_x, z and y are rows (b, d_in).
+ */
+ssm_status ssm_gated_state_update(float *state, const void *u, int64_t u_ld, const void *gate_a,
+                                  int64_t gate_a_ld, const void *gate_x, int64_t gate_x_ld,
+                                  const float *A, const float *bias_a, const float *bias_x,
+                                  const void *z, int64_t z_ld, void *y, int64_t y_ld, int64_t b,
+                                  int64_t d_in, ssm_dtype dtype, ssm_stream_t stream);
+
+/*
+ * Causal depthwise convolution over a sequence ("代码连连看——mamba", the conv
+ * in front of the SSM, which Mamba.step() takes one token at a time):
+ *     p = bias[d] + sum_j weight[d,j] * x[i, t - d_conv + 1 + j, d]
+ *     y[i,t,d] = silu ? p * sigmoid(p) : p
+ * Steps before the first come from conv_state, the window of
+ * ssm_conv_state_update: the last d_conv inputs, oldest first (its oldest entry
+ * is not read), zeros when NULL.  conv_state_out is the window after the last
+ * step, its entries from before the last sequence's start 0.
+ *
+ *   x, y            device rows (b L, d_in), dtype
+ *   weight          device fp32 (d_in, d_conv); tap j multiplies the j-th oldest
+ *   bias            device fp32 (d_in), nullable
+ *   conv_state      device (b, d_in, d_conv), dtype, nullable
+ *   conv_state_out  the same, nullable; may equal conv_state
+ *   d_conv          1 .. 8, else SSM_ERR_UNSUPPORTED
+ */
+ssm_status ssm_conv1d_fwd(const void *x, int64_t x_ld, const float *weight, const float *bias,
+                          int silu, const void *conv_state, void *conv_state_out,
+                          const uint8_t *seq_start, void *y, int64_t y_ld, int64_t b, int64_t L,
+                          int64_t d_in, int64_t d_conv, ssm_dtype dtype, ssm_stream_t stream);
+
+/*
+ * Gradients of sum dy * y for ssm_conv1d_fwd with the same inputs (conv_state
+ * is data: no gradient of it).  dx rows (b L, d_in), dtype; dweight fp32
+ * (d_in, d_conv), dbias fp32 (d_in), nullable; workspace device, 16-byte
+ * aligned, >= ssm_conv1d_bwd_workspace_bytes(...) bytes.
+ */
+ssm_status ssm_conv1d_bwd(const void *x, int64_t x_ld, const float *weight, const float *bias,
+                          int silu, const void *conv_state, const uint8_t *seq_start,
+                          const void *dy, int64_t dy_ld, void *dx, int64_t dx_ld, float *dweight,
+                          float *dbias, int64_t b, int64_t L, int64_t d_in, int64_t d_conv,
+                          ssm_dtype dtype, void *workspace, size_t workspace_bytes,
+                          ssm_stream_t stream);
+
+/* Bytes of ssm_conv1d_bwd's workspace on the current device; (size_t)-1 for invalid sizes. */
+size_t ssm_conv1d_bwd_workspace_bytes(int64_t b, int64_t L, int64_t d_in, int64_t d_conv);
+
+/*
+ * One token: conv_state (b, d_in, d_conv) is rolled one place and x (rows
+ * (b, d_in)) put last, in place; y as above from the new window.
+ */
+ssm_status ssm_conv1d_update(void *conv_state, const void *x, int64_t x_ld, const float *weight,
+                             const float *bias, int silu, void *y, int64_t y_ld, int64_t b,
+                             int64_t d_in, int64_t d_conv, ssm_dtype dtype, ssm_stream_t stream);
+
+/*
+ * Gated RMS norm of rows.  With rms(v) = v / sqrt(mean(v^2) + eps), the mean
+ * over each of `groups` equal groups of channels:
+ *     y = rms(x * silu(z)) * weight                 norm_before_gate == 0
+ *     y = rms(x) * weight * silu(z)                 norm_before_gate != 0
+ * and y = rms(x) * weight when z is NULL.
+ *
+ *   x, z, y    device rows (rows, d), dtype; z nullable
+ *   weight     device fp32 (d)
+ *   groups     divides d, else SSM_ERR_INVALID_ARG
+ *   eps        finite, >= 0
+ */
+ssm_status ssm_gated_norm_fwd(const void *x, int64_t x_ld, const void *z, int64_t z_ld,
+                              const float *weight, int64_t groups, float eps,
+                              int norm_before_gate, void *y, int64_t y_ld, int64_t rows, int64_t d,
+                              ssm_dtype dtype, ssm_stream_t stream);
+
+/*
+ * Gradients of sum dy * y for ssm_gated_norm_fwd with the same inputs: dx, dz
+ * (required with z) rows (rows, d), dtype, and dweight fp32 (d).  Nothing from
+ * the forward is kept.  workspace device, 16-byte aligned, >=
+ * ssm_gated_norm_bwd_workspace_bytes(...) bytes.
+ */
+ssm_status ssm_gated_norm_bwd(const void *x, int64_t x_ld, const void *z, int64_t z_ld,
+                              const float *weight, int64_t groups, float eps,
+                              int norm_before_gate, const void *dy, int64_t dy_ld, void *dx,
+                              int64_t dx_ld, void *dz, int64_t dz_ld, float *dweight, int64_t rows,
+                              int64_t d, ssm_dtype dtype, void *workspace, size_t workspace_bytes,
+                              ssm_stream_t stream);
+
+/* Bytes of ssm_gated_norm_bwd's workspace on the current device; (size_t)-1 for invalid sizes. */
+size_t ssm_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t d, int64_t groups);
+
+/*
+ * Between two blocks: the block's output x, normed (post_weight given) and
+ * scaled (scale given), is added to the residual, and the sum normed for the
+ * next block:
+ *     v = post_weight ? rms(x) * post_weight : x
+ *     residual_out = round(residual + (scale ? scale * v : v))
+ *     y = rms(residual_out) * weight
+ * (round: to residual_dtype; y is the norm of the rounded residual, the value
+ * that the next block and the backward read).
+ *
+ *   x, y                     device rows (rows, d), dtype
+ *   residual, residual_out   device rows (rows, d), residual_dtype (SSM_F32 or
+ *                            dtype); residual nullable (0, the first block);
+ *                            residual_out may be exactly residual (same stride)
+ *   weight, post_weight, scale   device fp32 (d); the last two nullable
+ */
+ssm_status ssm_add_norm_fwd(const void *x, int64_t x_ld, const void *residual, int64_t residual_ld,
+                            const float *weight, const float *post_weight, const float *scale,
+                            float eps, void *y, int64_t y_ld, void *residual_out,
+                            int64_t residual_out_ld, int64_t rows, int64_t d, ssm_dtype dtype,
+                            ssm_dtype residual_dtype, ssm_stream_t stream);
+
+/*
+ * Gradients of sum dy * y + sum dresidual_out * residual_out for
+ * ssm_add_norm_fwd, from residual_out as it wrote it (the rounding is passed
+ * through as the identity).
+ *
+ *   x                x of the forward; read when scale or post_weight is given
+ *                    (required then)
+ *   dy               rows (rows, d), dtype
+ *   dresidual_out    rows (rows, d), residual_dtype, nullable (0)
+ *   dx               rows (rows, d), dtype
+ *   dresidual        rows (rows, d), residual_dtype, nullable; may be exactly
+ *                    dresidual_out (same stride)
+ *   dweight          fp32 (d);  dpost_weight, dscale fp32 (d), required with
+ *                    post_weight / scale and not written without
+ *   workspace        device, 16-byte aligned, >= ssm_add_norm_bwd_workspace_bytes(...)
+ */
+ssm_status ssm_add_norm_bwd(const void *x, int64_t x_ld, const void *residual_out,
+                            int64_t residual_out_ld, const float *weight, const float *post_weight,
+                            const float *scale, float eps, const void *dy, int64_t dy_ld,
+                            const void *dresidual_out, int64_t dresidual_out_ld, void *dx,
+                            int64_t dx_ld, void *dresidual, int64_t dresidual_ld, float *dweight,
+                            float *dpost_weight, float *dscale, int64_t rows, int64_t d,
+                            ssm_dtype dtype, ssm_dtype residual_dtype, void *workspace,
+                            size_t workspace_bytes, ssm_stream_t stream);
+
+/* Bytes of ssm_add_norm_bwd's workspace on the current device; (size_t)-1 for invalid sizes. */
+size_t ssm_add_norm_bwd_workspace_bytes(int64_t rows, int64_t d);
 
 /*
  * Synchronises `stream` and returns SSM_OK, or SSM_ERR_CUDA with the CUDA

@@ -1,0 +1,647 @@
+// block_ops.cu -- the C ABI of the operators around the scan (gated
+// recurrence, causal convolution, norms): argument validation, kernel
+// selection and launch, under the rules of ssmscan.cu.
+#include <cmath>
+
+#include "abi_host.cuh"
+#include "conv1d.cuh"
+#include "gated_scan.cuh"
+#include "norms.cuh"
+
+using namespace ssm_host;
+
+namespace {
+
+cudaStream_t cu(ssm_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// A named argument as rows of `width` bytes, `pitch` bytes apart; contiguous
+// arguments are one row.
+struct RowSpan {
+  const char *name;
+  const void *p;
+  int64_t rows, width, pitch;
+};
+
+// Whether two arguments share a byte.  Rows of the same pitch may interleave
+// (the two halves of one projection's rows).
+bool rows_overlap(const RowSpan &a, const RowSpan &b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t a1 = a0 + (uintptr_t)((a.rows - 1) * a.pitch + a.width);
+  const uintptr_t b1 = b0 + (uintptr_t)((b.rows - 1) * b.pitch + b.width);
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (a.pitch != b.pitch) return true;
+  const int64_t off = a0 <= b0 ? (int64_t)((b0 - a0) % (uintptr_t)a.pitch)
+                               : (a.pitch - (int64_t)((a0 - b0) % (uintptr_t)a.pitch)) % a.pitch;
+  return off < a.width || a.pitch - off < b.width;
+}
+
+// Collects a call's arguments and checks them: presence, alignment, strides,
+// and that no output shares bytes with another argument.
+class Args {
+ public:
+  Args(const char *what, size_t es) : what_(what), es_(es) {}
+  // `rows` rows of `d` elements of `es` bytes, ld elements apart
+  void rows(bool out, const char *name, const void *p, int64_t rows, int64_t d, int64_t ld,
+            size_t es = 0) {
+    es = es ? es : es_;
+    if (!p) return;
+    if (status_ == SSM_OK && !aligned(p, es))
+      status_ = fail(SSM_ERR_INVALID_ARG, "%s: %s is not %zu-byte aligned", what_, name, es);
+    int64_t t;
+    if (status_ == SSM_OK && ld < d)
+      status_ = fail(SSM_ERR_INVALID_ARG, "%s: %s_ld %lld is below the row's %lld elements", what_,
+                     name, (long long)ld, (long long)d);
+    if (status_ == SSM_OK && (!mul_ok(rows, ld, &t) || t > INT64_MAX / 16))
+      status_ = fail(SSM_ERR_INVALID_ARG, "%s: the rows of %s overflow int64", what_, name);
+    add(out, {name, p, rows, d * (int64_t)es, ld * (int64_t)es});
+  }
+  void flat(bool out, const char *name, const void *p, int64_t bytes, size_t align = 4) {
+    if (!p) return;
+    if (status_ == SSM_OK && !aligned(p, align))
+      status_ = fail(SSM_ERR_INVALID_ARG, "%s: %s is not %zu-byte aligned", what_, name, align);
+    add(out, {name, p, 1, bytes, bytes});
+  }
+  // this output may be exactly this input
+  void same(const char *out, const char *in) {
+    same_out_ = out;
+    same_in_ = in;
+  }
+  ssm_status check() {
+    if (status_ != SSM_OK) return status_;
+    for (int i = 0; i < n_; ++i) {
+      if (!out_[i]) continue;
+      for (int j = 0; j < n_; ++j) {
+        if (j == i || (out_[j] && j < i)) continue;
+        const RowSpan &a = span_[i], &b = span_[j];
+        if (same_out_ && !strcmp(a.name, same_out_) && !strcmp(b.name, same_in_) && a.p == b.p &&
+            a.rows == b.rows && a.width == b.width && a.pitch == b.pitch)
+          continue;
+        if (rows_overlap(a, b))
+          return fail(SSM_ERR_INVALID_ARG, "%s: %s overlaps %s", what_, a.name, b.name);
+      }
+    }
+    return SSM_OK;
+  }
+
+ private:
+  void add(bool out, const RowSpan &s) {
+    if (n_ == kMax) {
+      status_ = fail(SSM_ERR_INVALID_ARG, "%s: too many arguments", what_);
+      return;
+    }
+    out_[n_] = out;
+    span_[n_++] = s;
+  }
+  static constexpr int kMax = 32;
+  const char *what_;
+  size_t es_;
+  ssm_status status_ = SSM_OK;
+  int n_ = 0;
+  bool out_[kMax];
+  RowSpan span_[kMax];
+  const char *same_out_ = nullptr, *same_in_ = nullptr;
+};
+
+ssm_status bad_dtype(const char *what, ssm_dtype t) {
+  return t == SSM_F32 || t == SSM_BF16 ? SSM_OK
+                                       : fail(SSM_ERR_UNSUPPORTED, "%s: unknown dtype %d", what, (int)t);
+}
+
+// Sizes of a call: none negative, their product (times 16 bytes) in int64.
+bool sizes_ok(std::initializer_list<int64_t> sizes) {
+  int64_t t = 16;
+  for (int64_t s : sizes) {
+    if (s < 0) return false;
+    if (s > 0 && !mul_ok(t, s, &t)) return false;
+  }
+  return true;
+}
+
+ssm_status zero(float *p, int64_t n, cudaStream_t st, const char *what) {
+  if (!p || n <= 0) return SSM_OK;
+  const cudaError_t e = cudaMemsetAsync(p, 0, (size_t)n * 4, st);
+  return e == cudaSuccess ? SSM_OK : fail(SSM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+ssm_status need_workspace(const char *what, const void *ws, size_t have, size_t need) {
+  if (need == 0) return SSM_OK;
+  if (!ws || have < need)
+    return fail(SSM_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws ? have : 0, need);
+  return SSM_OK;
+}
+
+// The parameters' gradients from n partial rows of m0 + m1 + m2 values.
+ssm_status col_sum(const float *part, int64_t n, int64_t m0, float *out0, int64_t m1, float *out1,
+                   int64_t m2, float *out2, cudaStream_t st, const char *what) {
+  const dim3 block(ssm::kColSumCols, ssm::kColSumRows);
+  const int64_t m = m0 + m1 + m2;
+  ssm::col_sum_kernel<<<(unsigned)((m + ssm::kColSumCols - 1) / ssm::kColSumCols), block, 0, st>>>(
+      ssm::ColSumParams{part, n, m0, m1, m2, out0, out1, out2});
+  return check_launch(what);
+}
+
+unsigned blocks_of(int64_t n, int threads) { return (unsigned)((n + threads - 1) / threads); }
+
+__global__ void copy_or_zero_f32(const float *src, float *dst, int64_t n) {
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * blockDim.x)
+    dst[i] = src ? src[i] : 0.0f;
+}
+
+// An empty sequence hands its start state (or zeros) through.
+ssm_status pass_state(const float *src, float *dst, int64_t n, cudaStream_t st, const char *what) {
+  if (!dst || src == dst || n <= 0) return SSM_OK;
+  copy_or_zero_f32<<<grid_for(n), 256, 0, st>>>(src, dst, n);
+  return check_launch(what);
+}
+
+// --------------------------------------------------------- gated recurrence
+int64_t gated_chunks(int64_t L) { return (L + ssm::kGatedChunk - 1) / ssm::kGatedChunk; }
+
+int64_t gated_bwd_parts(int64_t b, int64_t, int64_t) { return b; }
+
+ssm_status check_gated(const char *what, Args &a, const ssm::GatedParams &p, ssm_dtype dtype) {
+  if (ssm_status s = bad_dtype(what, dtype)) return s;
+  if (!sizes_ok({p.b, p.L, p.d}))
+    return fail(SSM_ERR_INVALID_ARG, "%s: negative size or sizes that overflow int64", what);
+  const int64_t R = p.b * p.L;
+  if (R > 0 && p.d > 0 && (!p.u || !p.ga || !p.gx || !p.A))
+    return fail(SSM_ERR_INVALID_ARG, "%s: u, gate_a, gate_x and A are required", what);
+  a.rows(false, "u", p.u, R, p.d, p.u_ld);
+  a.rows(false, "gate_a", p.ga, R, p.d, p.ga_ld);
+  a.rows(false, "gate_x", p.gx, R, p.d, p.gx_ld);
+  a.rows(false, "z", p.z, R, p.d, p.z_ld);
+  a.flat(false, "A", p.A, p.d * 4);
+  a.flat(false, "bias_a", p.ba, p.d * 4);
+  a.flat(false, "bias_x", p.bx, p.d * 4);
+  a.flat(false, "seq_start", p.start, R, 1);
+  return SSM_OK;
+}
+
+ssm_status check_states(const char *what, const void *p, size_t have, int64_t b, int64_t L, int64_t d) {
+  const size_t need = (size_t)(b * gated_chunks(L) * d) * 4;
+  if (have < need)
+    return fail(SSM_ERR_WORKSPACE, "%s: chunk_states of %zu bytes, %zu needed", what, have, need);
+  (void)p;
+  return SSM_OK;
+}
+
+// -------------------------------------------------------------- convolution
+int64_t conv_bwd_parts(int64_t b, int64_t, int64_t) { return b; }
+
+ssm_status check_conv(const char *what, Args &a, const ssm::ConvParams &p, int64_t K,
+                      ssm_dtype dtype) {
+  if (ssm_status s = bad_dtype(what, dtype)) return s;
+  if (K < 1 || K > ssm::kMaxConv)
+    return fail(SSM_ERR_UNSUPPORTED, "%s: d_conv %lld not in 1 .. %d", what, (long long)K, ssm::kMaxConv);
+  if (!sizes_ok({p.b, p.L, p.d, K}))
+    return fail(SSM_ERR_INVALID_ARG, "%s: negative size or sizes that overflow int64", what);
+  const int64_t R = p.b * p.L;
+  if (R > 0 && p.d > 0 && (!p.x || !p.w))
+    return fail(SSM_ERR_INVALID_ARG, "%s: x and weight are required", what);
+  a.rows(false, "x", p.x, R, p.d, p.x_ld);
+  a.flat(false, "weight", p.w, p.d * K * 4);
+  a.flat(false, "bias", p.bias, p.d * 4);
+  a.flat(false, "seq_start", p.start, R, 1);
+  return SSM_OK;
+}
+
+// -------------------------------------------------------------------- norms
+int64_t norm_bwd_parts(int64_t rows) {
+  const int64_t most = 4 * device_sms();
+  return rows < most ? rows : most;
+}
+
+ssm_status check_eps(const char *what, float eps) {
+  return std::isfinite(eps) && eps >= 0.0f
+             ? SSM_OK
+             : fail(SSM_ERR_INVALID_ARG, "%s: eps is negative or not finite", what);
+}
+
+ssm_status check_gated_norm(const char *what, Args &a, const ssm::GatedNormParams &p,
+                            ssm_dtype dtype) {
+  if (ssm_status s = bad_dtype(what, dtype)) return s;
+  if (!sizes_ok({p.rows, p.d}))
+    return fail(SSM_ERR_INVALID_ARG, "%s: negative size or sizes that overflow int64", what);
+  if (p.groups < 1 || p.d % p.groups != 0)
+    return fail(SSM_ERR_INVALID_ARG, "%s: groups %lld does not divide d %lld", what,
+                (long long)p.groups, (long long)p.d);
+  if (ssm_status s = check_eps(what, p.eps)) return s;
+  if (p.rows > 0 && p.d > 0 && (!p.x || !p.w))
+    return fail(SSM_ERR_INVALID_ARG, "%s: x and weight are required", what);
+  a.rows(false, "x", p.x, p.rows, p.d, p.x_ld);
+  a.rows(false, "z", p.z, p.rows, p.d, p.z_ld);
+  a.flat(false, "weight", p.w, p.d * 4);
+  return SSM_OK;
+}
+
+ssm_status check_add_norm(const char *what, Args &a, const ssm::AddNormParams &p, ssm_dtype dtype,
+                          ssm_dtype rdtype) {
+  if (ssm_status s = bad_dtype(what, dtype)) return s;
+  if (rdtype != SSM_F32 && rdtype != dtype)
+    return fail(SSM_ERR_UNSUPPORTED, "%s: residual_dtype %d is neither SSM_F32 nor dtype", what,
+                (int)rdtype);
+  if (!sizes_ok({p.rows, p.d, 3}))
+    return fail(SSM_ERR_INVALID_ARG, "%s: negative size or sizes that overflow int64", what);
+  if (ssm_status s = check_eps(what, p.eps)) return s;
+  if (p.rows > 0 && p.d > 0 && !p.w) return fail(SSM_ERR_INVALID_ARG, "%s: weight is required", what);
+  a.rows(false, "x", p.x, p.rows, p.d, p.x_ld);
+  a.flat(false, "weight", p.w, p.d * 4);
+  a.flat(false, "post_weight", p.post, p.d * 4);
+  a.flat(false, "scale", p.scale, p.d * 4);
+  return SSM_OK;
+}
+
+}  // namespace
+
+#ifdef SSM_DEBUG_BOUNDS
+cudaError_t ssm_host::take_block_bounds_word(unsigned int *word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_ssm_bounds_word, sizeof *word);
+  if (e == cudaSuccess && *word) {
+    const unsigned int none = 0;
+    e = cudaMemcpyToSymbol(g_ssm_bounds_word, &none, sizeof none);
+  }
+  return e;
+}
+#endif
+
+extern "C" {
+
+size_t ssm_gated_scan_states_bytes(int64_t b, int64_t L, int64_t d_in) {
+  if (!sizes_ok({b, L, d_in})) return (size_t)-1;
+  return (size_t)(b * gated_chunks(L) * d_in) * 4;
+}
+
+ssm_status ssm_gated_scan_fwd(const void *u, int64_t u_ld, const void *gate_a, int64_t gate_a_ld,
+                              const void *gate_x, int64_t gate_x_ld, const float *A,
+                              const float *bias_a, const float *bias_x, const void *z,
+                              int64_t z_ld, const uint8_t *seq_start, const float *h0,
+                              float *h_last, void *y, int64_t y_ld, float *chunk_states,
+                              size_t chunk_states_bytes, int64_t b, int64_t L, int64_t d_in,
+                              ssm_dtype dtype, ssm_stream_t stream) {
+  const char *what = "ssm_gated_scan_fwd";
+  g_last_error.clear();
+  ssm::GatedParams p{u,  gate_a, gate_x, z,      u_ld,         gate_a_ld, gate_x_ld, z_ld, A, bias_a,
+                     bias_x, seq_start, h0, h_last, y, y_ld, chunk_states, b, L, d_in};
+  Args a(what, esize(dtype));
+  if (ssm_status s = check_gated(what, a, p, dtype)) return s;
+  if (b * L > 0 && d_in > 0 && !y) return fail(SSM_ERR_INVALID_ARG, "%s: y is required", what);
+  a.flat(false, "h0", h0, b * d_in * 4);
+  a.flat(true, "h_last", h_last, b * d_in * 4);
+  a.rows(true, "y", y, b * L, d_in, y_ld);
+  a.flat(true, "chunk_states", chunk_states, b * gated_chunks(L) * d_in * 4);
+  a.same("h_last", "h0");
+  if (ssm_status s = a.check()) return s;
+  if (chunk_states)
+    if (ssm_status s = check_states(what, chunk_states, chunk_states_bytes, b, L, d_in)) return s;
+  if (b == 0 || d_in == 0) return ok();
+  if (L == 0) return pass_state(h0, h_last, b * d_in, cu(stream), what);
+  if (dtype == SSM_BF16)
+    ssm::gated_fwd_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p);
+  else
+    ssm::gated_fwd_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p);
+  return check_launch(what);
+}
+
+size_t ssm_gated_scan_bwd_workspace_bytes(int64_t b, int64_t L, int64_t d_in) {
+  if (!sizes_ok({b, L, d_in, 3})) return (size_t)-1;
+  return (size_t)(gated_bwd_parts(b, L, d_in) * 3 * d_in) * 4;
+}
+
+ssm_status ssm_gated_scan_bwd(const void *u, int64_t u_ld, const void *gate_a, int64_t gate_a_ld,
+                              const void *gate_x, int64_t gate_x_ld, const float *A,
+                              const float *bias_a, const float *bias_x, const void *z,
+                              int64_t z_ld, const uint8_t *seq_start, const void *dout,
+                              int64_t dout_ld, const float *dh_last, void *du, int64_t du_ld,
+                              void *dgate_a, int64_t dgate_a_ld, void *dgate_x,
+                              int64_t dgate_x_ld, void *dz, int64_t dz_ld, float *dA,
+                              float *dbias_a, float *dbias_x, float *dh0, int64_t b, int64_t L,
+                              int64_t d_in, ssm_dtype dtype, const float *chunk_states,
+                              size_t chunk_states_bytes, void *workspace, size_t workspace_bytes,
+                              ssm_stream_t stream) {
+  const char *what = "ssm_gated_scan_bwd";
+  g_last_error.clear();
+  if (!z) dz = nullptr;
+  ssm::GatedParams f{u,  gate_a, gate_x, z, u_ld, gate_a_ld, gate_x_ld, z_ld, A, bias_a, bias_x,
+                     seq_start, nullptr, nullptr, nullptr, 0, const_cast<float *>(chunk_states), b,
+                     L, d_in};
+  Args a(what, esize(dtype));
+  if (ssm_status s = check_gated(what, a, f, dtype)) return s;
+  const int64_t R = b * L;
+  if (R > 0 && d_in > 0 && (!dout || !du || !dgate_a || !dgate_x || !chunk_states || (z && !dz)))
+    return fail(SSM_ERR_INVALID_ARG, "%s: dout, du, dgate_a, dgate_x, chunk_states and, with z, dz "
+                "are required", what);
+  if (d_in > 0 && !dA) return fail(SSM_ERR_INVALID_ARG, "%s: dA is required", what);
+  const size_t need = ssm_gated_scan_bwd_workspace_bytes(b, L, d_in);
+  a.rows(false, "dout", dout, R, d_in, dout_ld);
+  a.flat(false, "dh_last", dh_last, b * d_in * 4);
+  a.flat(false, "chunk_states", chunk_states, b * gated_chunks(L) * d_in * 4);
+  a.rows(true, "du", du, R, d_in, du_ld);
+  a.rows(true, "dgate_a", dgate_a, R, d_in, dgate_a_ld);
+  a.rows(true, "dgate_x", dgate_x, R, d_in, dgate_x_ld);
+  a.rows(true, "dz", dz, R, d_in, dz_ld);
+  a.flat(true, "dA", dA, d_in * 4);
+  a.flat(true, "dbias_a", dbias_a, d_in * 4);
+  a.flat(true, "dbias_x", dbias_x, d_in * 4);
+  a.flat(true, "dh0", dh0, b * d_in * 4);
+  a.flat(true, "workspace", workspace, (int64_t)need, 16);
+  a.same("dh0", "dh_last");
+  if (ssm_status s = a.check()) return s;
+  const cudaStream_t st = cu(stream);
+  if (d_in == 0) return ok();
+  if (R == 0) {
+    for (float *g : {dA, dbias_a, dbias_x})
+      if (ssm_status s = zero(g, d_in, st, what)) return s;
+    return pass_state(dh_last, dh0, b * d_in, st, what);
+  }
+  if (ssm_status s = check_states(what, chunk_states, chunk_states_bytes, b, L, d_in)) return s;
+  if (ssm_status s = need_workspace(what, workspace, workspace_bytes, need)) return s;
+  float *part = static_cast<float *>(workspace);
+  ssm::GatedBwdParams q{f,  dout,  dout_ld, dh_last,    du,         dgate_a, dgate_x,
+                        dz, du_ld, dgate_a_ld, dgate_x_ld, dz_ld, dh0, part};
+  if (dtype == SSM_BF16)
+    ssm::gated_bwd_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, st>>>(q);
+  else
+    ssm::gated_bwd_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, st>>>(q);
+  if (ssm_status s = check_launch(what)) return s;
+  return col_sum(part, gated_bwd_parts(b, L, d_in), d_in, dA, d_in, dbias_a, d_in, dbias_x, st, what);
+}
+
+ssm_status ssm_gated_state_update(float *state, const void *u, int64_t u_ld, const void *gate_a,
+                                  int64_t gate_a_ld, const void *gate_x, int64_t gate_x_ld,
+                                  const float *A, const float *bias_a, const float *bias_x,
+                                  const void *z, int64_t z_ld, void *y, int64_t y_ld, int64_t b,
+                                  int64_t d_in, ssm_dtype dtype, ssm_stream_t stream) {
+  const char *what = "ssm_gated_state_update";
+  g_last_error.clear();
+  ssm::GatedParams p{u,  gate_a, gate_x, z, u_ld, gate_a_ld, gate_x_ld, z_ld, A, bias_a, bias_x,
+                     nullptr, nullptr, nullptr, y, y_ld, nullptr, b, 1, d_in};
+  Args a(what, esize(dtype));
+  if (ssm_status s = check_gated(what, a, p, dtype)) return s;
+  if (b > 0 && d_in > 0 && (!state || !y))
+    return fail(SSM_ERR_INVALID_ARG, "%s: state and y are required", what);
+  a.flat(true, "state", state, b * d_in * 4);
+  a.rows(true, "y", y, b, d_in, y_ld);
+  if (ssm_status s = a.check()) return s;
+  if (b == 0 || d_in == 0) return ok();
+  if (dtype == SSM_BF16)
+    ssm::gated_step_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p, state);
+  else
+    ssm::gated_step_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p, state);
+  return check_launch(what);
+}
+
+ssm_status ssm_conv1d_fwd(const void *x, int64_t x_ld, const float *weight, const float *bias,
+                          int silu, const void *conv_state, void *conv_state_out,
+                          const uint8_t *seq_start, void *y, int64_t y_ld, int64_t b, int64_t L,
+                          int64_t d_in, int64_t d_conv, ssm_dtype dtype, ssm_stream_t stream) {
+  const char *what = "ssm_conv1d_fwd";
+  g_last_error.clear();
+  ssm::ConvParams p{x, x_ld, weight, bias, silu != 0, conv_state, conv_state_out, seq_start, y, y_ld,
+                    b, L, d_in, (int)d_conv};
+  Args a(what, esize(dtype));
+  if (ssm_status s = check_conv(what, a, p, d_conv, dtype)) return s;
+  if (b * L > 0 && d_in > 0 && !y) return fail(SSM_ERR_INVALID_ARG, "%s: y is required", what);
+  const size_t es = esize(dtype);
+  a.flat(false, "conv_state", conv_state, b * d_in * d_conv * (int64_t)es, es);
+  a.flat(true, "conv_state_out", conv_state_out, b * d_in * d_conv * (int64_t)es, es);
+  a.rows(true, "y", y, b * L, d_in, y_ld);
+  a.same("conv_state_out", "conv_state");
+  if (ssm_status s = a.check()) return s;
+  if (b == 0 || d_in == 0 || (L == 0 && !conv_state_out)) return ok();
+  if (dtype == SSM_BF16)
+    ssm::conv_fwd_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p);
+  else
+    ssm::conv_fwd_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p);
+  return check_launch(what);
+}
+
+size_t ssm_conv1d_bwd_workspace_bytes(int64_t b, int64_t L, int64_t d_in, int64_t d_conv) {
+  if (d_conv < 1 || d_conv > ssm::kMaxConv || !sizes_ok({b, L, d_in, d_conv + 1})) return (size_t)-1;
+  return (size_t)(conv_bwd_parts(b, L, d_in) * d_in * (d_conv + 1)) * 4;
+}
+
+ssm_status ssm_conv1d_bwd(const void *x, int64_t x_ld, const float *weight, const float *bias,
+                          int silu, const void *conv_state, const uint8_t *seq_start,
+                          const void *dy, int64_t dy_ld, void *dx, int64_t dx_ld, float *dweight,
+                          float *dbias, int64_t b, int64_t L, int64_t d_in, int64_t d_conv,
+                          ssm_dtype dtype, void *workspace, size_t workspace_bytes,
+                          ssm_stream_t stream) {
+  const char *what = "ssm_conv1d_bwd";
+  g_last_error.clear();
+  ssm::ConvParams p{x, x_ld, weight, bias, silu != 0, conv_state, nullptr, seq_start, nullptr, 0, b, L,
+                    d_in, (int)d_conv};
+  Args a(what, esize(dtype));
+  if (ssm_status s = check_conv(what, a, p, d_conv, dtype)) return s;
+  const int64_t R = b * L;
+  if (R > 0 && d_in > 0 && (!dy || !dx))
+    return fail(SSM_ERR_INVALID_ARG, "%s: dy and dx are required", what);
+  if (d_in > 0 && !dweight) return fail(SSM_ERR_INVALID_ARG, "%s: dweight is required", what);
+  const size_t es = esize(dtype), need = ssm_conv1d_bwd_workspace_bytes(b, L, d_in, d_conv);
+  a.flat(false, "conv_state", conv_state, b * d_in * d_conv * (int64_t)es, es);
+  a.rows(false, "dy", dy, R, d_in, dy_ld);
+  a.rows(true, "dx", dx, R, d_in, dx_ld);
+  a.flat(true, "dweight", dweight, d_in * d_conv * 4);
+  a.flat(true, "dbias", dbias, d_in * 4);
+  a.flat(true, "workspace", workspace, (int64_t)need, 16);
+  if (ssm_status s = a.check()) return s;
+  const cudaStream_t st = cu(stream);
+  if (d_in == 0) return ok();
+  if (R == 0) {
+    if (ssm_status s = zero(dweight, d_in * d_conv, st, what)) return s;
+    return zero(dbias, d_in, st, what);
+  }
+  if (ssm_status s = need_workspace(what, workspace, workspace_bytes, need)) return s;
+  float *part = static_cast<float *>(workspace);
+  ssm::ConvBwdParams q{p, dy, dy_ld, dx, dx_ld, part};
+  if (dtype == SSM_BF16)
+    ssm::conv_bwd_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, st>>>(q);
+  else
+    ssm::conv_bwd_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, st>>>(q);
+  if (ssm_status s = check_launch(what)) return s;
+  return col_sum(part, conv_bwd_parts(b, L, d_in), d_in * d_conv, dweight, d_in, dbias, 0, nullptr, st,
+                 what);
+}
+
+ssm_status ssm_conv1d_update(void *conv_state, const void *x, int64_t x_ld, const float *weight,
+                             const float *bias, int silu, void *y, int64_t y_ld, int64_t b,
+                             int64_t d_in, int64_t d_conv, ssm_dtype dtype, ssm_stream_t stream) {
+  const char *what = "ssm_conv1d_update";
+  g_last_error.clear();
+  ssm::ConvParams p{x, x_ld, weight, bias, silu != 0, nullptr, nullptr, nullptr, y, y_ld, b, 1, d_in,
+                    (int)d_conv};
+  Args a(what, esize(dtype));
+  if (ssm_status s = check_conv(what, a, p, d_conv, dtype)) return s;
+  if (b > 0 && d_in > 0 && (!conv_state || !y))
+    return fail(SSM_ERR_INVALID_ARG, "%s: conv_state and y are required", what);
+  const size_t es = esize(dtype);
+  a.flat(true, "conv_state", conv_state, b * d_in * d_conv * (int64_t)es, es);
+  a.rows(true, "y", y, b, d_in, y_ld);
+  if (ssm_status s = a.check()) return s;
+  if (b == 0 || d_in == 0) return ok();
+  if (dtype == SSM_BF16)
+    ssm::conv_step_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p, conv_state);
+  else
+    ssm::conv_step_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p, conv_state);
+  return check_launch(what);
+}
+
+ssm_status ssm_gated_norm_fwd(const void *x, int64_t x_ld, const void *z, int64_t z_ld,
+                              const float *weight, int64_t groups, float eps,
+                              int norm_before_gate, void *y, int64_t y_ld, int64_t rows, int64_t d,
+                              ssm_dtype dtype, ssm_stream_t stream) {
+  const char *what = "ssm_gated_norm_fwd";
+  g_last_error.clear();
+  ssm::GatedNormParams p{x, z, x_ld, z_ld, weight, groups, eps, norm_before_gate != 0, y, y_ld, rows, d};
+  Args a(what, esize(dtype));
+  if (ssm_status s = check_gated_norm(what, a, p, dtype)) return s;
+  if (rows > 0 && d > 0 && !y) return fail(SSM_ERR_INVALID_ARG, "%s: y is required", what);
+  a.rows(true, "y", y, rows, d, y_ld);
+  if (ssm_status s = a.check()) return s;
+  if (rows == 0 || d == 0) return ok();
+  const int64_t n = rows * groups;
+  const unsigned grid = (unsigned)(n < (1 << 20) ? n : (1 << 20));
+  if (dtype == SSM_BF16)
+    ssm::gated_norm_fwd_kernel<__nv_bfloat16><<<grid, ssm::kNormThreads, 0, cu(stream)>>>(p);
+  else
+    ssm::gated_norm_fwd_kernel<float><<<grid, ssm::kNormThreads, 0, cu(stream)>>>(p);
+  return check_launch(what);
+}
+
+size_t ssm_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t d, int64_t groups) {
+  if (groups < 1 || !sizes_ok({rows, d}) || d % groups != 0) return (size_t)-1;
+  return (size_t)(norm_bwd_parts(rows) * d) * 4;
+}
+
+ssm_status ssm_gated_norm_bwd(const void *x, int64_t x_ld, const void *z, int64_t z_ld,
+                              const float *weight, int64_t groups, float eps,
+                              int norm_before_gate, const void *dy, int64_t dy_ld, void *dx,
+                              int64_t dx_ld, void *dz, int64_t dz_ld, float *dweight, int64_t rows,
+                              int64_t d, ssm_dtype dtype, void *workspace, size_t workspace_bytes,
+                              ssm_stream_t stream) {
+  const char *what = "ssm_gated_norm_bwd";
+  g_last_error.clear();
+  if (!z) dz = nullptr;
+  ssm::GatedNormParams p{x, z, x_ld, z_ld, weight, groups, eps, norm_before_gate != 0, nullptr, 0, rows, d};
+  Args a(what, esize(dtype));
+  if (ssm_status s = check_gated_norm(what, a, p, dtype)) return s;
+  if (rows > 0 && d > 0 && (!dy || !dx || (z && !dz)))
+    return fail(SSM_ERR_INVALID_ARG, "%s: dy, dx and, with z, dz are required", what);
+  if (d > 0 && !dweight) return fail(SSM_ERR_INVALID_ARG, "%s: dweight is required", what);
+  const size_t need = ssm_gated_norm_bwd_workspace_bytes(rows, d, groups);
+  a.rows(false, "dy", dy, rows, d, dy_ld);
+  a.rows(true, "dx", dx, rows, d, dx_ld);
+  a.rows(true, "dz", dz, rows, d, dz_ld);
+  a.flat(true, "dweight", dweight, d * 4);
+  a.flat(true, "workspace", workspace, (int64_t)need, 16);
+  if (ssm_status s = a.check()) return s;
+  const cudaStream_t st = cu(stream);
+  if (d == 0) return ok();
+  if (rows == 0) return zero(dweight, d, st, what);
+  if (ssm_status s = need_workspace(what, workspace, workspace_bytes, need)) return s;
+  float *part = static_cast<float *>(workspace);
+  const int64_t n = norm_bwd_parts(rows);
+  ssm::GatedNormBwdParams q{p, dy, dy_ld, dx, dz, dx_ld, dz_ld, part};
+  if (dtype == SSM_BF16)
+    ssm::gated_norm_bwd_kernel<__nv_bfloat16><<<(unsigned)n, ssm::kNormThreads, 0, st>>>(q);
+  else
+    ssm::gated_norm_bwd_kernel<float><<<(unsigned)n, ssm::kNormThreads, 0, st>>>(q);
+  if (ssm_status s = check_launch(what)) return s;
+  return col_sum(part, n, d, dweight, 0, nullptr, 0, nullptr, st, what);
+}
+
+ssm_status ssm_add_norm_fwd(const void *x, int64_t x_ld, const void *residual, int64_t residual_ld,
+                            const float *weight, const float *post_weight, const float *scale,
+                            float eps, void *y, int64_t y_ld, void *residual_out,
+                            int64_t residual_out_ld, int64_t rows, int64_t d, ssm_dtype dtype,
+                            ssm_dtype residual_dtype, ssm_stream_t stream) {
+  const char *what = "ssm_add_norm_fwd";
+  g_last_error.clear();
+  ssm::AddNormParams p{x, residual, x_ld, residual_ld, weight, post_weight, scale, eps, y, residual_out,
+                       y_ld, residual_out_ld, rows, d};
+  Args a(what, esize(dtype));
+  if (ssm_status s = check_add_norm(what, a, p, dtype, residual_dtype)) return s;
+  if (rows > 0 && d > 0 && (!x || !y || !residual_out))
+    return fail(SSM_ERR_INVALID_ARG, "%s: x, y and residual_out are required", what);
+  a.rows(false, "residual", residual, rows, d, residual_ld, esize(residual_dtype));
+  a.rows(true, "y", y, rows, d, y_ld);
+  a.rows(true, "residual_out", residual_out, rows, d, residual_out_ld, esize(residual_dtype));
+  a.same("residual_out", "residual");
+  if (ssm_status s = a.check()) return s;
+  if (rows == 0 || d == 0) return ok();
+  const unsigned grid = (unsigned)(rows < (1 << 20) ? rows : (1 << 20));
+  using bf16 = __nv_bfloat16;
+  if (dtype == SSM_F32)
+    ssm::add_norm_fwd_kernel<float, float><<<grid, ssm::kNormThreads, 0, cu(stream)>>>(p);
+  else if (residual_dtype == SSM_F32)
+    ssm::add_norm_fwd_kernel<bf16, float><<<grid, ssm::kNormThreads, 0, cu(stream)>>>(p);
+  else
+    ssm::add_norm_fwd_kernel<bf16, bf16><<<grid, ssm::kNormThreads, 0, cu(stream)>>>(p);
+  return check_launch(what);
+}
+
+size_t ssm_add_norm_bwd_workspace_bytes(int64_t rows, int64_t d) {
+  if (!sizes_ok({rows, d, 3})) return (size_t)-1;
+  return (size_t)(norm_bwd_parts(rows) * 3 * d) * 4;
+}
+
+ssm_status ssm_add_norm_bwd(const void *x, int64_t x_ld, const void *residual_out,
+                            int64_t residual_out_ld, const float *weight, const float *post_weight,
+                            const float *scale, float eps, const void *dy, int64_t dy_ld,
+                            const void *dresidual_out, int64_t dresidual_out_ld, void *dx,
+                            int64_t dx_ld, void *dresidual, int64_t dresidual_ld, float *dweight,
+                            float *dpost_weight, float *dscale, int64_t rows, int64_t d,
+                            ssm_dtype dtype, ssm_dtype residual_dtype, void *workspace,
+                            size_t workspace_bytes, ssm_stream_t stream) {
+  const char *what = "ssm_add_norm_bwd";
+  g_last_error.clear();
+  if (!post_weight) dpost_weight = nullptr;
+  if (!scale) dscale = nullptr;
+  if (!post_weight && !scale) x = nullptr;
+  ssm::AddNormParams p{x, nullptr, x_ld, 0, weight, post_weight, scale, eps, nullptr,
+                       const_cast<void *>(residual_out), 0, residual_out_ld, rows, d};
+  Args a(what, esize(dtype));
+  if (ssm_status s = check_add_norm(what, a, p, dtype, residual_dtype)) return s;
+  if (rows > 0 && d > 0 && (!residual_out || !dy || !dx || (!x && (post_weight || scale))))
+    return fail(SSM_ERR_INVALID_ARG,
+                "%s: residual_out, dy, dx and, with post_weight or scale, x are required", what);
+  if (d > 0 && (!dweight || (post_weight && !dpost_weight) || (scale && !dscale)))
+    return fail(SSM_ERR_INVALID_ARG,
+                "%s: dweight and, with post_weight / scale, their gradients are required", what);
+  const size_t rs = esize(residual_dtype), need = ssm_add_norm_bwd_workspace_bytes(rows, d);
+  a.rows(false, "residual_out", residual_out, rows, d, residual_out_ld, rs);
+  a.rows(false, "dy", dy, rows, d, dy_ld);
+  a.rows(false, "dresidual_out", dresidual_out, rows, d, dresidual_out_ld, rs);
+  a.rows(true, "dx", dx, rows, d, dx_ld);
+  a.rows(true, "dresidual", dresidual, rows, d, dresidual_ld, rs);
+  a.flat(true, "dweight", dweight, d * 4);
+  a.flat(true, "dpost_weight", dpost_weight, d * 4);
+  a.flat(true, "dscale", dscale, d * 4);
+  a.flat(true, "workspace", workspace, (int64_t)need, 16);
+  a.same("dresidual", "dresidual_out");
+  if (ssm_status s = a.check()) return s;
+  const cudaStream_t st = cu(stream);
+  if (d == 0) return ok();
+  if (rows == 0) {
+    for (float *g : {dweight, dpost_weight, dscale})
+      if (ssm_status s = zero(g, d, st, what)) return s;
+    return ok();
+  }
+  if (ssm_status s = need_workspace(what, workspace, workspace_bytes, need)) return s;
+  float *part = static_cast<float *>(workspace);
+  const int64_t n = norm_bwd_parts(rows);
+  ssm::AddNormBwdParams q{p, dy, dresidual_out, dy_ld, dresidual_out_ld, dx, dresidual, dx_ld,
+                          dresidual_ld, part};
+  using bf16 = __nv_bfloat16;
+  if (dtype == SSM_F32)
+    ssm::add_norm_bwd_kernel<float, float><<<(unsigned)n, ssm::kNormThreads, 0, st>>>(q);
+  else if (residual_dtype == SSM_F32)
+    ssm::add_norm_bwd_kernel<bf16, float><<<(unsigned)n, ssm::kNormThreads, 0, st>>>(q);
+  else
+    ssm::add_norm_bwd_kernel<bf16, bf16><<<(unsigned)n, ssm::kNormThreads, 0, st>>>(q);
+  if (ssm_status s = check_launch(what)) return s;
+  return col_sum(part, n, d, dweight, d, dpost_weight, d, dscale, st, what);
+}
+
+}  // extern "C"

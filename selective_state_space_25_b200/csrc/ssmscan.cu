@@ -3,126 +3,21 @@
 // arguments before it touches CUDA, never allocates, never synchronises
 // (except ssm_check_device_errors) and reports failures as ssm_status with a
 // per-thread message.
-#include <cstdarg>
-#include <cstdio>
-#include <cstring>
-#include <initializer_list>
 #include <mutex>
-#include <string>
 #include <type_traits>
 
-#include "ssmscan.h"
+#include "abi_host.cuh"
 #include "scan_bwd.cuh"
 #include "scan_fwd.cuh"
 #include "scan_ws.cuh"
 #include "ss2d_fwd.cuh"
 #include "state_update.cuh"
 
+using namespace ssm_host;
+
+thread_local std::string ssm_host::g_last_error;
+
 namespace {
-
-thread_local std::string g_last_error;
-
-ssm_status fail(ssm_status s, const char *fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return s;
-}
-
-ssm_status ok() { return SSM_OK; }
-
-bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
-
-bool supported_state(int64_t n) {
-  return n == 1 || n == 2 || n == 4 || n == 8 || n == 16 || n == 32 || n == 64;
-}
-
-size_t esize(ssm_dtype t) { return t == SSM_BF16 ? 2 : 4; }
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// A named byte range of one argument; NULL or empty ranges overlap nothing.
-struct Span {
-  const char *name;
-  const void *p;
-  int64_t bytes;
-};
-
-bool overlap(const Span &a, const Span &b) {
-  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + (uintptr_t)b.bytes && b0 < a0 + (uintptr_t)a.bytes;
-}
-
-// Outputs (and in-place buffers) must not overlap an input or each other.
-// same_out / same_in name one output allowed to be exactly the given input
-// (the same address: h_last == h0); any other overlap is an error.
-ssm_status check_disjoint(const char *what, std::initializer_list<Span> outs,
-                          std::initializer_list<Span> ins, const void *same_out = nullptr,
-                          const void *same_in = nullptr) {
-  for (const Span &o : outs) {
-    for (const Span &i : ins) {
-      if (same_out && o.p == same_out && i.p == same_in && o.p == i.p && o.bytes == i.bytes) continue;
-      if (overlap(o, i))
-        return fail(SSM_ERR_INVALID_ARG, "%s: %s overlaps the input %s", what, o.name, i.name);
-    }
-    for (const Span &o2 : outs)
-      if (&o2 != &o && overlap(o, o2))
-        return fail(SSM_ERR_INVALID_ARG, "%s: outputs %s and %s overlap", what, o.name, o2.name);
-  }
-  return SSM_OK;
-}
-
-ssm_status check_launch(const char *what) {
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(SSM_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
-  return ok();
-}
-
-// Launch with programmatic stream serialization: the kernel may start once
-// every block of the previous kernel in the stream has called
-// grid_dependents_launch (or exited), and calls grid_dependency_wait before
-// it reads that kernel's results.
-template <typename... KArgs, typename... Args>
-ssm_status launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, int smem,
-                            cudaStream_t st, const char *what, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return fail(SSM_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
-  }
-  return ok();
-}
-
-// Opt a kernel into > 48 KB of dynamic shared memory once per device.
-template <auto Kernel>
-ssm_status ensure_smem(int bytes, const char *what) {
-  static bool done[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
-    return fail(SSM_ERR_CUDA, "%s: cudaGetDevice failed", what);
-  if (!done[dev]) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess)
-      return fail(SSM_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", what, cudaGetErrorString(e));
-    done[dev] = true;
-  }
-  return ok();
-}
 
 // ------------------------------------------------------------ scan launch
 // Tile shape of the fast scan kernel: channels per CTA, steps per chunk,
@@ -210,26 +105,6 @@ ssm_status launch_scan_fast(const ssm::ScanParams &p, cudaStream_t st) {
 // States per scan thread of the warp-specialised kernel: 4 up to d_state 16,
 // 8 for 32 (four scan warps either way); 0 = not compiled for this d_state.
 constexpr int ws_states(int n) { return n == 8 || n == 16 ? 4 : (n == 32 ? 8 : 0); }
-
-// SMs of the current device (148 on B200; also the answer when no device is
-// visible, so the workspace query works on a host without a GPU).
-int device_sms() {
-  static int cached[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-    cudaGetLastError();
-    return 148;
-  }
-  if (!cached[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-      cudaGetLastError();
-      n = 148;
-    }
-    cached[dev] = n;
-  }
-  return cached[dev];
-}
 
 // Split of the sequence into blocks (scan_ws.cuh, split scan) for problems
 // whose b * ceil(d_in / 32) CTAs would leave more than half of the SMs idle:
@@ -419,11 +294,6 @@ ssm_status check_step_args(const char *what, float *ssm_state, const void *x, co
   return check_disjoint(what, {{"ssm_state", ssm_state, ns}, {"y", y, na}},
                         {{"x", x, na}, {"dt", dt, na}, {"z", z, na}, {"B", B, nbc}, {"C", C, nbc},
                          {"A", A, np * d_state}, {"D", D, np}, {"dt_bias", dt_bias, np}});
-}
-
-unsigned grid_for(int64_t n) {
-  const int64_t blocks = (n + 255) / 256;
-  return (unsigned)(blocks < 148 * 32 ? (blocks > 0 ? blocks : 1) : 148 * 32);
 }
 
 // ------------------------------------------------------------ SS2D launch
@@ -1333,8 +1203,11 @@ ssm_status ssm_check_device_errors(ssm_stream_t stream) {
 #ifdef SSM_DEBUG_BOUNDS
   unsigned int w = 0;
   e = cudaMemcpyFromSymbol(&w, g_ssm_bounds_word, sizeof w);
+  unsigned int w_block = 0;  // each source file's kernels have a word of their own
+  if (e == cudaSuccess) e = take_block_bounds_word(&w_block);
   if (e != cudaSuccess)
     return fail(SSM_ERR_CUDA, "ssm_check_device_errors: %s", cudaGetErrorString(e));
+  w |= w_block;
   if (w) {
     const unsigned int zero = 0;
     e = cudaMemcpyToSymbol(g_ssm_bounds_word, &zero, sizeof zero);

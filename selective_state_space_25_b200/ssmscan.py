@@ -85,6 +85,46 @@ _lib.ss2d_cross_scan_ex.restype = _INT
 _lib.ss2d_cross_merge_ex.argtypes = [_P, _P] + [_I64] * 4 + [_INT, _INT, _P]
 _lib.ss2d_cross_merge_ex.restype = _INT
 SS2D_ORDERS = {"cross": 0, "snake": 1}
+_ROWS = [_P, _I64]  # an activation and its row stride
+_lib.ssm_gated_scan_states_bytes.argtypes = [_I64] * 3
+_lib.ssm_gated_scan_states_bytes.restype = _SZ
+_lib.ssm_gated_scan_fwd.argtypes = (_ROWS * 3 + [_P] * 3 + _ROWS + [_P] * 3 + _ROWS + [_P, _SZ]
+                                    + [_I64] * 3 + [_INT, _P])
+_lib.ssm_gated_scan_fwd.restype = _INT
+_lib.ssm_gated_scan_bwd_workspace_bytes.argtypes = [_I64] * 3
+_lib.ssm_gated_scan_bwd_workspace_bytes.restype = _SZ
+_lib.ssm_gated_scan_bwd.argtypes = (_ROWS * 3 + [_P] * 3 + _ROWS + [_P] + _ROWS + [_P] + _ROWS * 4
+                                    + [_P] * 4 + [_I64] * 3 + [_INT, _P, _SZ, _P, _SZ, _P])
+_lib.ssm_gated_scan_bwd.restype = _INT
+_lib.ssm_gated_state_update.argtypes = ([_P] + _ROWS * 3 + [_P] * 3 + _ROWS * 2 + [_I64] * 2
+                                        + [_INT, _P])
+_lib.ssm_gated_state_update.restype = _INT
+_lib.ssm_conv1d_fwd.argtypes = (_ROWS + [_P, _P, _INT] + [_P] * 3 + _ROWS + [_I64] * 4 + [_INT, _P])
+_lib.ssm_conv1d_fwd.restype = _INT
+_lib.ssm_conv1d_bwd_workspace_bytes.argtypes = [_I64] * 4
+_lib.ssm_conv1d_bwd_workspace_bytes.restype = _SZ
+_lib.ssm_conv1d_bwd.argtypes = (_ROWS + [_P, _P, _INT] + [_P] * 2 + _ROWS * 2 + [_P] * 2 + [_I64] * 4
+                                + [_INT, _P, _SZ, _P])
+_lib.ssm_conv1d_bwd.restype = _INT
+_lib.ssm_conv1d_update.argtypes = [_P] + _ROWS + [_P, _P, _INT] + _ROWS + [_I64] * 3 + [_INT, _P]
+_lib.ssm_conv1d_update.restype = _INT
+_F32 = ctypes.c_float
+_lib.ssm_gated_norm_fwd.argtypes = (_ROWS * 2 + [_P, _I64, _F32, _INT] + _ROWS + [_I64] * 2
+                                    + [_INT, _P])
+_lib.ssm_gated_norm_fwd.restype = _INT
+_lib.ssm_gated_norm_bwd_workspace_bytes.argtypes = [_I64] * 3
+_lib.ssm_gated_norm_bwd_workspace_bytes.restype = _SZ
+_lib.ssm_gated_norm_bwd.argtypes = (_ROWS * 2 + [_P, _I64, _F32, _INT] + _ROWS * 3 + [_P]
+                                    + [_I64] * 2 + [_INT, _P, _SZ, _P])
+_lib.ssm_gated_norm_bwd.restype = _INT
+_lib.ssm_add_norm_fwd.argtypes = (_ROWS * 2 + [_P] * 3 + [_F32] + _ROWS * 2 + [_I64] * 2
+                                  + [_INT, _INT, _P])
+_lib.ssm_add_norm_fwd.restype = _INT
+_lib.ssm_add_norm_bwd_workspace_bytes.argtypes = [_I64] * 2
+_lib.ssm_add_norm_bwd_workspace_bytes.restype = _SZ
+_lib.ssm_add_norm_bwd.argtypes = (_ROWS * 2 + [_P] * 3 + [_F32] + _ROWS * 4 + [_P] * 3 + [_I64] * 2
+                                  + [_INT, _INT, _P, _SZ, _P])
+_lib.ssm_add_norm_bwd.restype = _INT
 _lib.ssm_check_device_errors.argtypes = [_P]
 _lib.ssm_check_device_errors.restype = _INT
 _lib.ssm_debug_bounds_enabled.argtypes = []
@@ -411,6 +451,465 @@ def ss2d_cross_merge(ys, H, W, y=None, stream=None, order="cross"):
     _check(_lib.ss2d_cross_merge_ex(_ptr(ys), _ptr(y), b, H, W, d_in, SS2D_ORDERS[order],
                                     _dtype_code(ys), _stream(stream)), "ss2d_cross_merge")
     return y
+
+
+# ------------------------------------------------- around the scan
+# Activations of these calls may have strided rows: the last dimension
+# adjacent, the leading ones collapsible to rows a fixed stride apart (a half of
+# a projection's output).  The calls run on the inputs' device whatever the
+# current one is; what they allocate comes from the pool of the stream they run
+# on.
+
+def _device_of(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: on {t.device}, expected a CUDA device")
+    return t.device
+
+
+def _rows(t, name, shape, dtype, device):
+    """(pointer, row stride) of an activation; (None, 0) without one."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    d = shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), d
+    st = t.stride()
+    if d > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: its last dimension must be adjacent")
+    ld, span = None, None  # the rows' stride, from the innermost leading dimension longer than 1
+    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = span = s
+        elif s != span:
+            raise ValueError(f"{name}: its rows must be a fixed stride apart")
+        span *= n
+    if ld is None:
+        ld = d
+    if ld < d:
+        raise ValueError(f"{name}: its rows overlap (stride {ld} for {d} elements)")
+    return t.data_ptr(), ld
+
+
+def _launch(fn, where, device, stream, *args):
+    """Calls the library on `device` and `stream` (None: its current one)."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if device.index == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status != SSM_OK:
+        raise SsmError(status, where, last_error())
+
+
+class _Pool:
+    """Allocates on the stream a call runs on, so that memory the caching
+    allocator hands out is not still in use on another one."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            self.stream = torch.cuda.ExternalStream(int(stream), device=device)
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def _workspace(workspace, nbytes, pool):
+    """(tensor, pointer, bytes) of the given workspace, or of one from the pool
+    for the bytes the library asks for on its device."""
+    if workspace is None:
+        with torch.cuda.device(pool.device):
+            workspace = pool.empty(max(int(nbytes()), 1), torch.uint8)
+    else:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace: expected a torch.Tensor")
+        if workspace.device != pool.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: must be contiguous on {pool.device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def ssm_gated_scan_states_bytes(b: int, L: int, d_in: int) -> int:
+    return int(_lib.ssm_gated_scan_states_bytes(b, L, d_in))
+
+
+def ssm_gated_scan_bwd_workspace_bytes(b: int, L: int, d_in: int) -> int:
+    return int(_lib.ssm_gated_scan_bwd_workspace_bytes(b, L, d_in))
+
+
+def _gated_inputs(u, gate_a, gate_x, A, bias_a, bias_x, z, shape, dev):
+    act, d = u.dtype, shape[-1]
+    f32 = torch.float32
+    _need(A, "A", (d,), f32, dev)
+    _need(bias_a, "bias_a", (d,), f32, dev)
+    _need(bias_x, "bias_x", (d,), f32, dev)
+    return (*_rows(u, "u", shape, act, dev), *_rows(gate_a, "gate_a", shape, act, dev),
+            *_rows(gate_x, "gate_x", shape, act, dev), _ptr(A), _ptr(bias_a), _ptr(bias_x),
+            *_rows(z, "z", shape, act, dev))
+
+
+def _chunk_states(states, name, b, L, d, dev):
+    if states is None:
+        return None, 0
+    if not isinstance(states, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if states.device != dev or not states.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous on {dev}")
+    return states.data_ptr(), states.numel() * states.element_size()
+
+
+def ssm_gated_scan_fwd(u, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, seq_start=None,
+                       h0=None, h_last=None, y=None, chunk_states=None, stream=None):
+    """Gated linear recurrence (see include/ssmscan.h).  u, gate_a, gate_x, z:
+    (b, L, d_in); A, bias_a, bias_x: (d_in,) fp32; seq_start: (b, L) uint8;
+    h0, h_last: (b, d_in) fp32.  Returns y (b, L, d_in).  With
+    ``chunk_states`` (a device buffer of ssm_gated_scan_states_bytes(...)
+    bytes) the states that ssm_gated_scan_bwd starts from are kept."""
+    dev = _device_of(u, "u")
+    if u.dim() != 3:
+        raise ValueError("u must be (b, L, d_in)")
+    shape = u.shape
+    b, L, d = shape
+    code = _dtype_code(u)
+    ins = _gated_inputs(u, gate_a, gate_x, A, bias_a, bias_x, z, shape, dev)
+    _need(seq_start, "seq_start", (b, L), torch.uint8, dev)
+    _need(h0, "h0", (b, d), torch.float32, dev)
+    _need(h_last, "h_last", (b, d), torch.float32, dev)
+    states = _chunk_states(chunk_states, "chunk_states", b, L, d, dev)
+    if y is None:
+        y = _Pool(dev, stream).empty(shape, u.dtype)
+    _launch(_lib.ssm_gated_scan_fwd, "ssm_gated_scan_fwd", dev, stream, *ins, _ptr(seq_start),
+            _ptr(h0), _ptr(h_last), *_rows(y, "y", shape, u.dtype, dev), *states, b, L, d, code)
+    return y
+
+
+def _outputs(out, spec, pool, dev):
+    """The outputs named in spec ({name: (shape, dtype, strided)}), from
+    ``out`` where it has them, else new."""
+    got = {}
+    for name, (shape, dtype, strided) in spec.items():
+        t = None if out is None else out.get(name)
+        if t is None:
+            t = pool.empty(shape, dtype)
+        elif not strided:
+            _need(t, name, shape, dtype, dev)
+        got[name] = t
+    return got
+
+
+def ssm_gated_scan_bwd(u, gate_a, gate_x, A, dout, states, bias_a=None, bias_x=None, z=None,
+                       seq_start=None, dh_last=None, want_dh0=False, workspace=None, stream=None,
+                       out=None):
+    """Gradients of sum(dout * y) [+ sum(dh_last * h_last)] for
+    ssm_gated_scan_fwd with the same inputs, from the ``chunk_states`` it
+    filled.  Returns a dict: du, dgate_a, dgate_x, dz (activation dtype; dz
+    only with z); dA, dbias_a, dbias_x (d_in,) fp32 (the biases' only with
+    them); dh0 (b, d_in) fp32 when want_dh0.  ``out``: a dict of tensors to
+    write into, by those names."""
+    dev = _device_of(u, "u")
+    if u.dim() != 3:
+        raise ValueError("u must be (b, L, d_in)")
+    shape, act, f32 = u.shape, u.dtype, torch.float32
+    b, L, d = shape
+    code = _dtype_code(u)
+    ins = _gated_inputs(u, gate_a, gate_x, A, bias_a, bias_x, z, shape, dev)
+    _need(seq_start, "seq_start", (b, L), torch.uint8, dev)
+    _need(dh_last, "dh_last", (b, d), f32, dev)
+    if states is None:
+        raise TypeError("states: expected the chunk_states of ssm_gated_scan_fwd")
+    states = _chunk_states(states, "states", b, L, d, dev)
+    pool = _Pool(dev, stream)
+    rows = ["du", "dgate_a", "dgate_x"] + (["dz"] if z is not None else [])
+    spec = {k: (shape, act, True) for k in rows}
+    spec["dA"] = ((d,), f32, False)
+    spec.update({"d" + k: ((d,), f32, False) for k, on in (("bias_a", bias_a), ("bias_x", bias_x))
+                 if on is not None})
+    if want_dh0:
+        spec["dh0"] = ((b, d), f32, False)
+    g = _outputs(out, spec, pool, dev)
+    ws, ws_ptr, ws_bytes = _workspace(
+        workspace, lambda: _lib.ssm_gated_scan_bwd_workspace_bytes(b, L, d), pool)
+    grads = [v for k in ("du", "dgate_a", "dgate_x", "dz")
+             for v in _rows(g.get(k), k, shape, act, dev)]
+    _launch(_lib.ssm_gated_scan_bwd, "ssm_gated_scan_bwd", dev, stream, *ins, _ptr(seq_start),
+            *_rows(dout, "dout", shape, act, dev), _ptr(dh_last), *grads, _ptr(g["dA"]),
+            _ptr(g.get("dbias_a")), _ptr(g.get("dbias_x")), _ptr(g.get("dh0")), b, L, d, code,
+            *states, ws_ptr, ws_bytes)
+    return g
+
+
+def ssm_gated_state_update(state, u, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, y=None,
+                           stream=None):
+    """One token of the gated recurrence; state (b, d_in) fp32 is updated in
+    place.  u, gate_a, gate_x, z: (b, d_in).  Returns y (b, d_in)."""
+    dev = _device_of(u, "u")
+    if u.dim() != 2:
+        raise ValueError("u must be (b, d_in)")
+    shape = u.shape
+    code = _dtype_code(u)
+    ins = _gated_inputs(u, gate_a, gate_x, A, bias_a, bias_x, z, shape, dev)
+    if state is None:
+        raise TypeError("state: expected a torch.Tensor")
+    _need(state, "state", shape, torch.float32, dev)
+    if y is None:
+        y = _Pool(dev, stream).empty(shape, u.dtype)
+    _launch(_lib.ssm_gated_state_update, "ssm_gated_state_update", dev, stream, _ptr(state), *ins,
+            *_rows(y, "y", shape, u.dtype, dev), shape[0], shape[1], code)
+    return y
+
+
+def _conv_inputs(x, weight, bias, shape, dev):
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be (d_in, d_conv)")
+    d, K = shape[-1], weight.shape[1]
+    _need(weight, "weight", (d, K), torch.float32, dev)
+    _need(bias, "bias", (d,), torch.float32, dev)
+    return _rows(x, "x", shape, x.dtype, dev), K
+
+
+def ssm_conv1d_fwd(x, weight, bias=None, silu=True, conv_state=None, conv_state_out=None,
+                   seq_start=None, y=None, stream=None):
+    """Causal depthwise convolution over a sequence (see include/ssmscan.h).
+    x: (b, L, d_in); weight: (d_in, d_conv) fp32; bias: (d_in,) fp32;
+    conv_state (the window in front of the first step), conv_state_out (the
+    one behind the last; may be conv_state): (b, d_in, d_conv) in x's dtype;
+    seq_start: (b, L) uint8.  Returns y (b, L, d_in)."""
+    dev = _device_of(x, "x")
+    if x.dim() != 3:
+        raise ValueError("x must be (b, L, d_in)")
+    shape = x.shape
+    b, L, d = shape
+    code = _dtype_code(x)
+    xr, K = _conv_inputs(x, weight, bias, shape, dev)
+    _need(conv_state, "conv_state", (b, d, K), x.dtype, dev)
+    _need(conv_state_out, "conv_state_out", (b, d, K), x.dtype, dev)
+    _need(seq_start, "seq_start", (b, L), torch.uint8, dev)
+    if y is None:
+        y = _Pool(dev, stream).empty(shape, x.dtype)
+    _launch(_lib.ssm_conv1d_fwd, "ssm_conv1d_fwd", dev, stream, *xr, _ptr(weight), _ptr(bias),
+            int(bool(silu)), _ptr(conv_state), _ptr(conv_state_out), _ptr(seq_start),
+            *_rows(y, "y", shape, x.dtype, dev), b, L, d, K, code)
+    return y
+
+
+def ssm_conv1d_bwd_workspace_bytes(b: int, L: int, d_in: int, d_conv: int) -> int:
+    return int(_lib.ssm_conv1d_bwd_workspace_bytes(b, L, d_in, d_conv))
+
+
+def ssm_conv1d_bwd(x, weight, dy, bias=None, silu=True, conv_state=None, seq_start=None,
+                   workspace=None, stream=None, out=None):
+    """Gradients of sum(dy * y) for ssm_conv1d_fwd with the same inputs:
+    a dict of dx (b, L, d_in), dweight (d_in, d_conv) fp32 and, with a bias,
+    dbias (d_in,) fp32.  ``out``: a dict of tensors to write into."""
+    dev = _device_of(x, "x")
+    if x.dim() != 3:
+        raise ValueError("x must be (b, L, d_in)")
+    shape, act, f32 = x.shape, x.dtype, torch.float32
+    b, L, d = shape
+    code = _dtype_code(x)
+    xr, K = _conv_inputs(x, weight, bias, shape, dev)
+    _need(conv_state, "conv_state", (b, d, K), act, dev)
+    _need(seq_start, "seq_start", (b, L), torch.uint8, dev)
+    pool = _Pool(dev, stream)
+    spec = dict(dx=(shape, act, True), dweight=((d, K), f32, False))
+    if bias is not None:
+        spec["dbias"] = ((d,), f32, False)
+    g = _outputs(out, spec, pool, dev)
+    ws, ws_ptr, ws_bytes = _workspace(
+        workspace, lambda: _lib.ssm_conv1d_bwd_workspace_bytes(b, L, d, K), pool)
+    _launch(_lib.ssm_conv1d_bwd, "ssm_conv1d_bwd", dev, stream, *xr, _ptr(weight), _ptr(bias),
+            int(bool(silu)), _ptr(conv_state), _ptr(seq_start), *_rows(dy, "dy", shape, act, dev),
+            *_rows(g["dx"], "dx", shape, act, dev), _ptr(g["dweight"]), _ptr(g.get("dbias")), b, L, d,
+            K, code, ws_ptr, ws_bytes)
+    return g
+
+
+def ssm_conv1d_update(conv_state, x, weight, bias=None, silu=True, y=None, stream=None):
+    """One token of the convolution; conv_state (b, d_in, d_conv) in x's dtype
+    is rolled and x (b, d_in) put last, in place.  Returns y (b, d_in)."""
+    dev = _device_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be (b, d_in)")
+    shape = x.shape
+    code = _dtype_code(x)
+    xr, K = _conv_inputs(x, weight, bias, shape, dev)
+    if conv_state is None:
+        raise TypeError("conv_state: expected a torch.Tensor")
+    _need(conv_state, "conv_state", (*shape, K), x.dtype, dev)
+    if y is None:
+        y = _Pool(dev, stream).empty(shape, x.dtype)
+    _launch(_lib.ssm_conv1d_update, "ssm_conv1d_update", dev, stream, _ptr(conv_state), *xr,
+            _ptr(weight), _ptr(bias), int(bool(silu)), *_rows(y, "y", shape, x.dtype, dev), shape[0],
+            shape[1], K, code)
+    return y
+
+
+def _row_count(shape):
+    n = 1
+    for s in shape[:-1]:
+        n *= s
+    return n
+
+
+def ssm_gated_norm_fwd(x, z, weight, groups=1, eps=1e-5, norm_before_gate=False, y=None, stream=None):
+    """RMS norm over `groups` groups of channels with the SiLU gate z (None:
+    no gate): rms(x silu(z)) weight, or rms(x) weight silu(z) with
+    norm_before_gate.  x, z: (..., d); weight: (d,) fp32.  Returns y like x."""
+    dev = _device_of(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must be (..., d)")
+    shape, act = x.shape, x.dtype
+    d = shape[-1]
+    code = _dtype_code(x)
+    xr, zr = _rows(x, "x", shape, act, dev), _rows(z, "z", shape, act, dev)
+    _need(weight, "weight", (d,), torch.float32, dev)
+    if y is None:
+        y = _Pool(dev, stream).empty(shape, act)
+    _launch(_lib.ssm_gated_norm_fwd, "ssm_gated_norm_fwd", dev, stream, *xr, *zr, _ptr(weight), groups,
+            eps, int(bool(norm_before_gate)), *_rows(y, "y", shape, act, dev), _row_count(shape), d,
+            code)
+    return y
+
+
+def ssm_gated_norm_bwd_workspace_bytes(rows: int, d: int, groups: int = 1) -> int:
+    return int(_lib.ssm_gated_norm_bwd_workspace_bytes(rows, d, groups))
+
+
+def ssm_gated_norm_bwd(x, z, weight, dy, groups=1, eps=1e-5, norm_before_gate=False, workspace=None,
+                       stream=None, out=None):
+    """Gradients of sum(dy * y) for ssm_gated_norm_fwd with the same inputs: a
+    dict of dx, dz (with z) like x, and dweight (d,) fp32.  ``out``: a dict of
+    tensors to write into."""
+    dev = _device_of(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must be (..., d)")
+    shape, act = x.shape, x.dtype
+    d, rows = shape[-1], _row_count(shape)
+    code = _dtype_code(x)
+    xr, zr = _rows(x, "x", shape, act, dev), _rows(z, "z", shape, act, dev)
+    _need(weight, "weight", (d,), torch.float32, dev)
+    dyr = _rows(dy, "dy", shape, act, dev)
+    pool = _Pool(dev, stream)
+    spec = dict(dx=(shape, act, True), dweight=((d,), torch.float32, False))
+    if z is not None:
+        spec["dz"] = (shape, act, True)
+    g = _outputs(out, spec, pool, dev)
+    ws, ws_ptr, ws_bytes = _workspace(
+        workspace, lambda: _lib.ssm_gated_norm_bwd_workspace_bytes(rows, d, groups), pool)
+    _launch(_lib.ssm_gated_norm_bwd, "ssm_gated_norm_bwd", dev, stream, *xr, *zr, _ptr(weight), groups,
+            eps, int(bool(norm_before_gate)), *dyr, *_rows(g["dx"], "dx", shape, act, dev),
+            *_rows(g.get("dz"), "dz", shape, act, dev), _ptr(g["dweight"]), rows, d, code, ws_ptr,
+            ws_bytes)
+    return g
+
+
+def ssm_add_norm_fwd(x, residual, weight, scale=None, post_weight=None, eps=1e-5,
+                     residual_dtype=None, y=None, residual_out=None, stream=None):
+    """residual_out = residual + scale * (post_weight ? rms(x) * post_weight : x)
+    and y = rms(residual_out) * weight.  x: (..., d); residual the same in
+    fp32 or x's dtype, or None (0); weight, scale, post_weight: (d,) fp32.
+    residual_dtype: of residual_out without a residual (default x's).
+    Returns (y, residual_out); residual_out may be residual."""
+    dev = _device_of(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must be (..., d)")
+    shape, act, f32 = x.shape, x.dtype, torch.float32
+    d = shape[-1]
+    code = _dtype_code(x)
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor):
+            raise TypeError("residual: expected a torch.Tensor")
+        if residual_dtype is not None and residual_dtype != residual.dtype:
+            raise TypeError(f"residual: dtype {residual.dtype}, expected {residual_dtype}")
+        residual_dtype = residual.dtype
+    elif residual_dtype is None:
+        residual_dtype = act if residual_out is None else residual_out.dtype
+    if residual_dtype != f32 and residual_dtype != act:
+        raise TypeError(f"residual dtype {residual_dtype}: expected fp32 or {act}")
+    rcode = SSM_F32 if residual_dtype == f32 else SSM_BF16
+    xr = _rows(x, "x", shape, act, dev)
+    rr = _rows(residual, "residual", shape, residual_dtype, dev)
+    _need(weight, "weight", (d,), f32, dev)
+    _need(scale, "scale", (d,), f32, dev)
+    _need(post_weight, "post_weight", (d,), f32, dev)
+    pool = _Pool(dev, stream)
+    if y is None:
+        y = pool.empty(shape, act)
+    if residual_out is None:
+        residual_out = pool.empty(shape, residual_dtype)
+    _launch(_lib.ssm_add_norm_fwd, "ssm_add_norm_fwd", dev, stream, *xr, *rr, _ptr(weight),
+            _ptr(post_weight), _ptr(scale), eps, *_rows(y, "y", shape, act, dev),
+            *_rows(residual_out, "residual_out", shape, residual_dtype, dev), _row_count(shape), d,
+            code, rcode)
+    return y, residual_out
+
+
+def ssm_add_norm_bwd_workspace_bytes(rows: int, d: int) -> int:
+    return int(_lib.ssm_add_norm_bwd_workspace_bytes(rows, d))
+
+
+def ssm_add_norm_bwd(x, residual_out, weight, dy, dresidual_out=None, scale=None, post_weight=None,
+                     eps=1e-5, want_dresidual=True, workspace=None, stream=None, out=None):
+    """Gradients of sum(dy * y) [+ sum(dresidual_out * residual_out)] for
+    ssm_add_norm_fwd, from the residual_out it wrote: a dict of dx, dresidual
+    (in residual_out's dtype, unless not wanted), dweight and, where given,
+    dscale, dpost_weight (d,) fp32.  x may be None without scale and
+    post_weight.  ``out``: a dict of tensors to write into; its dresidual may
+    be dresidual_out."""
+    dev = _device_of(dy, "dy")
+    if dy.dim() < 1:
+        raise ValueError("dy must be (..., d)")
+    shape, act, f32 = dy.shape, dy.dtype, torch.float32
+    d, rows = shape[-1], _row_count(shape)
+    code = _dtype_code(dy)
+    if not isinstance(residual_out, torch.Tensor):
+        raise TypeError("residual_out: expected a torch.Tensor")
+    res = residual_out.dtype
+    if res != f32 and res != act:
+        raise TypeError(f"residual dtype {res}: expected fp32 or {act}")
+    if x is None and (scale is not None or post_weight is not None):
+        raise TypeError("x: expected a torch.Tensor with scale or post_weight")
+    xr = _rows(x, "x", shape, act, dev)
+    rr = _rows(residual_out, "residual_out", shape, res, dev)
+    _need(weight, "weight", (d,), f32, dev)
+    _need(scale, "scale", (d,), f32, dev)
+    _need(post_weight, "post_weight", (d,), f32, dev)
+    dyr = _rows(dy, "dy", shape, act, dev)
+    dror = _rows(dresidual_out, "dresidual_out", shape, res, dev)
+    pool = _Pool(dev, stream)
+    spec = dict(dx=(shape, act, True), dweight=((d,), f32, False))
+    if want_dresidual:
+        spec["dresidual"] = (shape, res, True)
+    for k, on in (("dpost_weight", post_weight), ("dscale", scale)):
+        if on is not None:
+            spec[k] = ((d,), f32, False)
+    g = _outputs(out, spec, pool, dev)
+    ws, ws_ptr, ws_bytes = _workspace(
+        workspace, lambda: _lib.ssm_add_norm_bwd_workspace_bytes(rows, d), pool)
+    _launch(_lib.ssm_add_norm_bwd, "ssm_add_norm_bwd", dev, stream, *xr, *rr, _ptr(weight),
+            _ptr(post_weight), _ptr(scale), eps, *dyr, *dror, *_rows(g["dx"], "dx", shape, act, dev),
+            *_rows(g.get("dresidual"), "dresidual", shape, res, dev), _ptr(g["dweight"]),
+            _ptr(g.get("dpost_weight")), _ptr(g.get("dscale")), rows, d, code,
+            SSM_F32 if res == f32 else SSM_BF16, ws_ptr, ws_bytes)
+    return g
 
 
 def check_device_errors(stream=None) -> None:
