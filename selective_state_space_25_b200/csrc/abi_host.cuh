@@ -87,11 +87,11 @@ inline ssm_status check_launch(const char *what) {
 // grid_dependents_launch (or exited), and calls grid_dependency_wait before
 // it reads that kernel's results.
 template <typename... KArgs, typename... Args>
-ssm_status launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, int smem,
+ssm_status launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 threads, int smem,
                             cudaStream_t st, const char *what, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
+  cfg.blockDim = threads;
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -71,6 +71,113 @@ __device__ __forceinline__ void decay2(float2 x, float2 &a, float2 &w) {
   w.y = max_nan(w.y, 0.0f);
 }
 
+// ------------------------------------------------------- element access
+// VEC adjacent elements of an activation as one access (VEC * sizeof(T) bytes,
+// so aligned), in fp32 registers.  `n`: elements of the buffer up to the end of
+// its last row, for the debug-bounds build.
+template <typename T, int VEC> struct VecWord;
+template <> struct VecWord<__nv_bfloat16, 1> { using type = uint16_t; };
+template <> struct VecWord<__nv_bfloat16, 2> { using type = uint32_t; };
+template <> struct VecWord<__nv_bfloat16, 4> { using type = uint2; };
+template <> struct VecWord<__nv_bfloat16, 8> { using type = uint4; };
+template <> struct VecWord<float, 1> { using type = float; };
+template <> struct VecWord<float, 2> { using type = float2; };
+template <> struct VecWord<float, 4> { using type = float4; };
+
+template <typename T, int VEC>
+__device__ __forceinline__ typename VecWord<T, VEC>::type ld_raw(const void *p, int64_t i,
+                                                                 int64_t n) {
+  using W = typename VecWord<T, VEC>::type;
+  if (in_bounds(i, n - (VEC - 1), kBndAct))
+    return *reinterpret_cast<const W *>(static_cast<const T *>(p) + i);
+  return W{};
+}
+// The same through the non-coherent path, for data no one writes meanwhile.
+template <typename T, int VEC>
+__device__ __forceinline__ typename VecWord<T, VEC>::type ld_raw_ro(const void *p, int64_t i,
+                                                                    int64_t n) {
+  using W = typename VecWord<T, VEC>::type;
+  if (in_bounds(i, n - (VEC - 1), kBndAct))
+    return __ldg(reinterpret_cast<const W *>(static_cast<const T *>(p) + i));
+  return W{};
+}
+__device__ __forceinline__ void unpack(uint16_t w, float *v) { v[0] = bf16lo(w); }
+__device__ __forceinline__ void unpack(uint32_t w, float *v) {
+  v[0] = bf16lo(w);
+  v[1] = bf16hi(w);
+}
+__device__ __forceinline__ void unpack(uint2 w, float *v) {
+  unpack(w.x, v);
+  unpack(w.y, v + 2);
+}
+__device__ __forceinline__ void unpack(uint4 w, float *v) {
+  unpack(w.x, v);
+  unpack(w.y, v + 2);
+  unpack(w.z, v + 4);
+  unpack(w.w, v + 6);
+}
+__device__ __forceinline__ void unpack(float w, float *v) { v[0] = w; }
+__device__ __forceinline__ void unpack(float2 w, float *v) {
+  v[0] = w.x;
+  v[1] = w.y;
+}
+__device__ __forceinline__ void unpack(float4 w, float *v) {
+  v[0] = w.x;
+  v[1] = w.y;
+  v[2] = w.z;
+  v[3] = w.w;
+}
+// VEC values rounded once to T and stored as one access.
+template <typename T, int VEC>
+__device__ __forceinline__ void st_vec(void *p, int64_t i, int64_t n, const float *v) {
+  using W = typename VecWord<T, VEC>::type;
+  if (!in_bounds(i, n - (VEC - 1), kBndAct)) return;
+  T *q = static_cast<T *>(p) + i;
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (VEC == 1) *q = v[0];
+    if constexpr (VEC == 2) *reinterpret_cast<W *>(q) = make_float2(v[0], v[1]);
+    if constexpr (VEC == 4) *reinterpret_cast<W *>(q) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    if constexpr (VEC == 1) *q = __float2bfloat16_rn(v[0]);
+    if constexpr (VEC == 2) *reinterpret_cast<W *>(q) = pack_bf16x2(v[0], v[1]);
+    if constexpr (VEC == 4)
+      *reinterpret_cast<W *>(q) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    if constexpr (VEC == 8)
+      *reinterpret_cast<W *>(q) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+}
+// acc += a * b over VEC values, two to an instruction (packed fp32: the same
+// rate a lane, half the issue slots).
+template <int VEC>
+__device__ __forceinline__ void fma_vec(float *acc, const float *a, const float *b) {
+  if constexpr (VEC % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const float2 r = __ffma2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]),
+                                  make_float2(acc[e], acc[e + 1]));
+      acc[e] = r.x;
+      acc[e + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = fmaf(a[e], b[e], acc[e]);
+  }
+}
+
+__device__ __forceinline__ float ld_param(const float *p, int64_t i, int64_t n) {
+  return in_bounds(i, n, kBndParam) ? __ldg(p + i) : 0.0f;
+}
+
+// Elements from a buffer's first to the end of its last row.
+__device__ __forceinline__ int64_t extent(int64_t rows, int64_t d, int64_t ld) {
+  return (rows - 1) * ld + d;
+}
+
+__device__ __forceinline__ float sigmoid_f32(float x) {
+  return rcp_approx(1.0f + ex2_approx(-x * kLog2e));
+}
+
 // Sums of partial rows, the last step of the parameters' gradients: column c
 // of the m0 + m1 + m2 columns is sum_n part[n, c], taken by eight lanes in
 // order of n and then over the lanes (the same bits every time); it goes to
@@ -86,6 +193,7 @@ __global__ void col_sum_kernel(const ColSumParams p) {
   const int64_t m = p.m0 + p.m1 + p.m2;
   const int64_t c = blockIdx.x * (int64_t)kColSumCols + threadIdx.x;
   float acc = 0.0f;
+  grid_dependency_wait();
   if (c < m) {
 #pragma unroll 4
     for (int64_t i = threadIdx.y; i < p.n; i += kColSumRows)

@@ -2,6 +2,8 @@
 // recurrence, causal convolution, norms): argument validation, kernel
 // selection and launch, under the rules of ssmscan.cu.
 #include <cmath>
+#include <type_traits>
+#include <utility>
 
 #include "abi_host.cuh"
 #include "conv1d.cuh"
@@ -136,9 +138,9 @@ ssm_status col_sum(const float *part, int64_t n, int64_t m0, float *out0, int64_
                    int64_t m2, float *out2, cudaStream_t st, const char *what) {
   const dim3 block(ssm::kColSumCols, ssm::kColSumRows);
   const int64_t m = m0 + m1 + m2;
-  ssm::col_sum_kernel<<<(unsigned)((m + ssm::kColSumCols - 1) / ssm::kColSumCols), block, 0, st>>>(
-      ssm::ColSumParams{part, n, m0, m1, m2, out0, out1, out2});
-  return check_launch(what);
+  // may start while the kernel that writes the partial rows ends
+  return launch_dependent(ssm::col_sum_kernel, dim3((unsigned)((m + ssm::kColSumCols - 1) / ssm::kColSumCols)),
+                          block, 0, st, what, ssm::ColSumParams{part, n, m0, m1, m2, out0, out1, out2});
 }
 
 unsigned blocks_of(int64_t n, int threads) { return (unsigned)((n + threads - 1) / threads); }
@@ -188,7 +190,138 @@ ssm_status check_states(const char *what, const void *p, size_t have, int64_t b,
 }
 
 // -------------------------------------------------------------- convolution
-int64_t conv_bwd_parts(int64_t b, int64_t, int64_t) { return b; }
+// Whether rows of T can be read VEC elements at a time.
+bool vec_rows(int64_t vec, size_t es, int64_t d, std::initializer_list<std::pair<const void *, int64_t>> rows) {
+  if (d % vec != 0) return false;
+  for (const auto &r : rows)
+    if (r.first && (!aligned(r.first, vec * es) || r.second % vec != 0)) return false;
+  return true;
+}
+
+// Shape of the convolution's CTAs: `lanes` channel groups of VEC that fit a
+// warp, 256 / lanes segments of T steps.  A CTA's time goes as T plus the rows a
+// segment reads of its neighbours and its prologue (some 16 rows' worth), so T is
+// the multiple of 8 with the least of it over the waves of `occ` CTAs an SM.
+// Backward the CTAs of one wave loop over the segments instead, since each
+// writes a partial row of the parameters' gradients.
+struct ConvPlan {
+  int lanes, ctiles, T;
+  int64_t segs, blocks;  // CTAs along the segments
+};
+ConvPlan conv_plan(int64_t b, int64_t L, int64_t d, int vec, int occ, bool one_wave) {
+  ConvPlan best{};
+  int64_t least = -1;
+  ConvPlan c{};
+  const int64_t G = d > 0 ? (d + vec - 1) / vec : 1;
+  c.lanes = 1;
+  while (c.lanes < 32 && c.lanes < G) c.lanes *= 2;
+  c.ctiles = (int)((G + c.lanes - 1) / c.lanes);
+  const int64_t slots = ssm::kConvThreads / c.lanes;
+  const int64_t room = occ * (int64_t)device_sms();
+  const int64_t parts = room / c.ctiles > 0 ? room / c.ctiles : 1;
+  for (c.T = 8; c.T <= 128; c.T += 8) {
+    c.segs = L > 0 ? (L + c.T - 1) / c.T : 1;
+    c.blocks = (b * c.segs + slots - 1) / slots;
+    int64_t waves;
+    if (one_wave) {
+      waves = c.blocks > 0 ? (c.blocks + parts - 1) / parts : 1;
+      c.blocks = (c.blocks + waves - 1) / waves;
+      if (parts == 1) waves *= (c.ctiles + room - 1) / room;
+    } else {
+      waves = (c.blocks * c.ctiles + room - 1) / room;
+    }
+    const int64_t cost = waves * (c.T + 16);
+    if (least < 0 || cost < least) least = cost, best = c;
+  }
+  return best;
+}
+int64_t conv_bwd_parts(int64_t b, int64_t L, int64_t d) {  // of whichever kernel the call takes
+  int64_t most = 0;
+  for (int vec : {1, ssm::kConvBwdVec})
+    for (int occ : {2, 3}) {
+      const int64_t n = conv_plan(b, L, d, vec, occ, true).blocks;
+      if (n > most) most = n;
+    }
+  return most;
+}
+
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
+template <typename T, int K, int VEC>
+ssm_status launch_conv_fwd(ssm::ConvParams p, cudaStream_t st) {
+  const ConvPlan c = conv_plan(p.b, p.L, p.d, VEC, ssm::conv_fwd_occ(K), false);
+  p.lanes = c.lanes, p.ctiles = c.ctiles, p.T = c.T, p.segs = c.segs;
+  if (c.blocks > kMaxGrid / c.ctiles)
+    return fail(SSM_ERR_UNSUPPORTED, "ssm_conv1d_fwd: b * L * d_in too large for one grid");
+  const unsigned grid = (unsigned)(c.blocks * c.ctiles);
+  if (p.start)
+    ssm::conv_fwd_kernel<T, K, VEC, true><<<grid, ssm::kConvThreads, 0, st>>>(p);
+  else
+    ssm::conv_fwd_kernel<T, K, VEC, false><<<grid, ssm::kConvThreads, 0, st>>>(p);
+  return check_launch("ssm_conv1d_fwd");
+}
+
+template <typename T, int K, int VEC>
+ssm_status launch_conv_bwd(ssm::ConvBwdParams q, int64_t *parts, cudaStream_t st) {
+  const ConvPlan c = conv_plan(q.f.b, q.f.L, q.f.d, VEC, ssm::conv_bwd_occ(K, sizeof(T)), true);
+  q.f.lanes = c.lanes, q.f.ctiles = c.ctiles, q.f.T = c.T, q.f.segs = c.segs;
+  q.parts = (int)c.blocks;
+  *parts = c.blocks;
+  const unsigned grid = (unsigned)(c.blocks * c.ctiles);
+  if (q.f.start)
+    ssm::conv_bwd_kernel<T, K, VEC, true><<<grid, ssm::kConvThreads, 0, st>>>(q);
+  else
+    ssm::conv_bwd_kernel<T, K, VEC, false><<<grid, ssm::kConvThreads, 0, st>>>(q);
+  return check_launch("ssm_conv1d_bwd");
+}
+
+template <typename T, int K, int VEC>
+ssm_status launch_conv_step(const ssm::ConvParams &p, void *win, cudaStream_t st) {
+  const int64_t n = p.b * (p.d / VEC), blocks = (n + ssm::kConvThreads - 1) / ssm::kConvThreads;
+  if (blocks > kMaxGrid)
+    return fail(SSM_ERR_UNSUPPORTED, "ssm_conv1d_update: b * d_in too large for one grid");
+  ssm::conv_step_kernel<T, K, VEC><<<(unsigned)blocks, ssm::kConvThreads, 0, st>>>(p, win);
+  return check_launch("ssm_conv1d_update");
+}
+
+template <typename T, int K>
+ssm_status conv_fwd_k(const ssm::ConvParams &p, cudaStream_t st) {
+  constexpr int VEC = ssm::kConvVec;
+  if (vec_rows(VEC, sizeof(T), p.d, {{p.x, p.x_ld}, {p.y, p.y_ld}}) && aligned(p.w, 16))
+    return launch_conv_fwd<T, K, VEC>(p, st);
+  return launch_conv_fwd<T, K, 1>(p, st);
+}
+template <typename T, int K>
+ssm_status conv_bwd_k(const ssm::ConvBwdParams &q, int64_t *parts, cudaStream_t st) {
+  constexpr int VEC = ssm::kConvBwdVec;
+  if (vec_rows(VEC, sizeof(T), q.f.d, {{q.f.x, q.f.x_ld}, {q.dy, q.dy_ld}, {q.dx, q.dx_ld}}) &&
+      aligned(q.f.w, 16))
+    return launch_conv_bwd<T, K, VEC>(q, parts, st);
+  return launch_conv_bwd<T, K, 1>(q, parts, st);
+}
+template <typename T, int K>
+ssm_status conv_step_k(const ssm::ConvParams &p, void *win, cudaStream_t st) {
+  if (vec_rows(4, sizeof(T), p.d, {{p.x, p.x_ld}, {p.y, p.y_ld}}) && aligned(win, 16) && aligned(p.w, 16))
+    return launch_conv_step<T, K, 4>(p, win, st);
+  return launch_conv_step<T, K, 1>(p, win, st);
+}
+
+// f.template operator()<T, K>() for the call's type and width
+template <typename F> ssm_status conv_dispatch(ssm_dtype t, int64_t K, F &&f) {
+  const auto by_k = [&](auto type) -> ssm_status {
+    switch (K) {
+      case 1: return f(type, std::integral_constant<int, 1>());
+      case 2: return f(type, std::integral_constant<int, 2>());
+      case 3: return f(type, std::integral_constant<int, 3>());
+      case 4: return f(type, std::integral_constant<int, 4>());
+      case 5: return f(type, std::integral_constant<int, 5>());
+      case 6: return f(type, std::integral_constant<int, 6>());
+      case 7: return f(type, std::integral_constant<int, 7>());
+      default: return f(type, std::integral_constant<int, 8>());
+    }
+  };
+  return t == SSM_BF16 ? by_k(__nv_bfloat16()) : by_k(float());
+}
 
 ssm_status check_conv(const char *what, Args &a, const ssm::ConvParams &p, int64_t K,
                       ssm_dtype dtype) {
@@ -399,7 +532,7 @@ ssm_status ssm_conv1d_fwd(const void *x, int64_t x_ld, const float *weight, cons
   const char *what = "ssm_conv1d_fwd";
   g_last_error.clear();
   ssm::ConvParams p{x, x_ld, weight, bias, silu != 0, conv_state, conv_state_out, seq_start, y, y_ld,
-                    b, L, d_in, (int)d_conv};
+                    b, L, d_in};
   Args a(what, esize(dtype));
   if (ssm_status s = check_conv(what, a, p, d_conv, dtype)) return s;
   if (b * L > 0 && d_in > 0 && !y) return fail(SSM_ERR_INVALID_ARG, "%s: y is required", what);
@@ -410,11 +543,9 @@ ssm_status ssm_conv1d_fwd(const void *x, int64_t x_ld, const float *weight, cons
   a.same("conv_state_out", "conv_state");
   if (ssm_status s = a.check()) return s;
   if (b == 0 || d_in == 0 || (L == 0 && !conv_state_out)) return ok();
-  if (dtype == SSM_BF16)
-    ssm::conv_fwd_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p);
-  else
-    ssm::conv_fwd_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p);
-  return check_launch(what);
+  return conv_dispatch(dtype, d_conv, [&](auto t, auto k) {
+    return conv_fwd_k<decltype(t), decltype(k)::value>(p, cu(stream));
+  });
 }
 
 size_t ssm_conv1d_bwd_workspace_bytes(int64_t b, int64_t L, int64_t d_in, int64_t d_conv) {
@@ -431,7 +562,7 @@ ssm_status ssm_conv1d_bwd(const void *x, int64_t x_ld, const float *weight, cons
   const char *what = "ssm_conv1d_bwd";
   g_last_error.clear();
   ssm::ConvParams p{x, x_ld, weight, bias, silu != 0, conv_state, nullptr, seq_start, nullptr, 0, b, L,
-                    d_in, (int)d_conv};
+                    d_in};
   Args a(what, esize(dtype));
   if (ssm_status s = check_conv(what, a, p, d_conv, dtype)) return s;
   const int64_t R = b * L;
@@ -454,13 +585,13 @@ ssm_status ssm_conv1d_bwd(const void *x, int64_t x_ld, const float *weight, cons
   }
   if (ssm_status s = need_workspace(what, workspace, workspace_bytes, need)) return s;
   float *part = static_cast<float *>(workspace);
-  ssm::ConvBwdParams q{p, dy, dy_ld, dx, dx_ld, part};
-  if (dtype == SSM_BF16)
-    ssm::conv_bwd_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, st>>>(q);
-  else
-    ssm::conv_bwd_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, st>>>(q);
-  if (ssm_status s = check_launch(what)) return s;
-  return col_sum(part, conv_bwd_parts(b, L, d_in), d_in * d_conv, dweight, d_in, dbias, 0, nullptr, st,
+  ssm::ConvBwdParams q{p, dy, dy_ld, dx, dx_ld, 0, part};
+  int64_t parts = 0;
+  if (ssm_status s = conv_dispatch(dtype, d_conv, [&](auto t, auto k) {
+        return conv_bwd_k<decltype(t), decltype(k)::value>(q, &parts, st);
+      }))
+    return s;
+  return col_sum(part, parts, d_in * d_conv, dweight, d_in, dbias, 0, nullptr, st,
                  what);
 }
 
@@ -469,8 +600,7 @@ ssm_status ssm_conv1d_update(void *conv_state, const void *x, int64_t x_ld, cons
                              int64_t d_in, int64_t d_conv, ssm_dtype dtype, ssm_stream_t stream) {
   const char *what = "ssm_conv1d_update";
   g_last_error.clear();
-  ssm::ConvParams p{x, x_ld, weight, bias, silu != 0, nullptr, nullptr, nullptr, y, y_ld, b, 1, d_in,
-                    (int)d_conv};
+  ssm::ConvParams p{x, x_ld, weight, bias, silu != 0, nullptr, nullptr, nullptr, y, y_ld, b, 1, d_in};
   Args a(what, esize(dtype));
   if (ssm_status s = check_conv(what, a, p, d_conv, dtype)) return s;
   if (b > 0 && d_in > 0 && (!conv_state || !y))
@@ -480,11 +610,9 @@ ssm_status ssm_conv1d_update(void *conv_state, const void *x, int64_t x_ld, cons
   a.rows(true, "y", y, b, d_in, y_ld);
   if (ssm_status s = a.check()) return s;
   if (b == 0 || d_in == 0) return ok();
-  if (dtype == SSM_BF16)
-    ssm::conv_step_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p, conv_state);
-  else
-    ssm::conv_step_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p, conv_state);
-  return check_launch(what);
+  return conv_dispatch(dtype, d_conv, [&](auto t, auto k) {
+    return conv_step_k<decltype(t), decltype(k)::value>(p, conv_state, cu(stream));
+  });
 }
 
 ssm_status ssm_gated_norm_fwd(const void *x, int64_t x_ld, const void *z, int64_t z_ld,

@@ -43,10 +43,6 @@ __device__ __forceinline__ void act_store(void *p, int64_t i, int64_t n, float v
   if (in_bounds(i, n, kBndAct)) Elem<T>::store(static_cast<T *>(p), i, v);
 }
 
-__device__ __forceinline__ float sigmoid_f32(float x) {
-  return rcp_approx(1.0f + ex2_approx(-x * kLog2e));
-}
-
 __device__ __forceinline__ GatedGate gated_gate(float ga, float gx, float A2) {
   GatedGate o;
   o.r = sigmoid_f32(ga);

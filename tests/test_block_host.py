@@ -150,6 +150,10 @@ def test_size_queries():
               L.ssm_gated_norm_bwd_workspace_bytes(2, 8, 3), L.ssm_gated_norm_bwd_workspace_bytes(2, 8, 0),
               L.ssm_add_norm_bwd_workspace_bytes(-1, 8), L.ssm_add_norm_bwd_workspace_bytes(2 ** 40, 2 ** 40)):
         assert q == NONE
+    for s in [(0, 5, 8), (2, 0, 8), (2, 5, 0), (0, 0, 0)]:  # empty problems have a size too
+        assert S.ssm_gated_scan_bwd_workspace_bytes(*s) >= 0 and S.ssm_conv1d_bwd_workspace_bytes(*s, 4) >= 0
+        assert S.ssm_gated_norm_bwd_workspace_bytes(s[0], s[2]) >= 0
+        assert S.ssm_add_norm_bwd_workspace_bytes(s[0], s[2]) >= 0
     # whole partial rows of the parameters' gradients
     assert S.ssm_gated_scan_bwd_workspace_bytes(2, 100, 24) % (3 * 24 * 4) == 0
     assert S.ssm_conv1d_bwd_workspace_bytes(2, 100, 24, 4) % (5 * 24 * 4) == 0
