@@ -143,8 +143,6 @@ ssm_status col_sum(const float *part, int64_t n, int64_t m0, float *out0, int64_
                           block, 0, st, what, ssm::ColSumParams{part, n, m0, m1, m2, out0, out1, out2});
 }
 
-unsigned blocks_of(int64_t n, int threads) { return (unsigned)((n + threads - 1) / threads); }
-
 __global__ void copy_or_zero_f32(const float *src, float *dst, int64_t n) {
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
        i += (int64_t)gridDim.x * blockDim.x)
@@ -158,10 +156,126 @@ ssm_status pass_state(const float *src, float *dst, int64_t n, cudaStream_t st, 
   return check_launch(what);
 }
 
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
+// Whether rows of T can be read VEC elements at a time.
+bool vec_rows(int64_t vec, size_t es, int64_t d, std::initializer_list<std::pair<const void *, int64_t>> rows) {
+  if (d % vec != 0) return false;
+  for (const auto &r : rows)
+    if (r.first && (!aligned(r.first, vec * es) || r.second % vec != 0)) return false;
+  return true;
+}
+
 // --------------------------------------------------------- gated recurrence
 int64_t gated_chunks(int64_t L) { return (L + ssm::kGatedChunk - 1) / ssm::kGatedChunk; }
 
-int64_t gated_bwd_parts(int64_t b, int64_t, int64_t) { return b; }
+// CTAs of a cluster, each a tile of 64 steps at a time.  An SM's time goes as the
+// CTAs it gets times the rounds of tiles each takes; the smallest cluster within
+// a tenth of the least (each doubling costs a wider exchange).
+struct GatedPlan {
+  int ctiles, csize;
+};
+GatedPlan gated_plan(int64_t b, int64_t L, int64_t d, int channels) {
+  const int64_t tiles = gated_chunks(L), sms = device_sms();
+  GatedPlan g;
+  g.ctiles = (int)((d + channels - 1) / channels);
+  int64_t cost[4], least = -1;
+  for (int k = 0; k < 4; ++k) {
+    const int64_t c = 1 << k;
+    cost[k] = ((b * g.ctiles * c + sms - 1) / sms) * ((tiles + c - 1) / c);
+    if (least < 0 || cost[k] < least) least = cost[k];
+  }
+  int k = 0;
+  while (10 * cost[k] > 11 * least) ++k;
+  g.csize = 1 << k;
+  return g;
+}
+int64_t gated_bwd_parts(int64_t b, int64_t L, int64_t d) {  // of whichever type
+  const int f = gated_plan(b, L, d, 32).csize, h = gated_plan(b, L, d, 64).csize;
+  return b * (f > h ? f : h);
+}
+
+template <auto Kernel, typename P>
+ssm_status launch_gated(const P &p, int64_t b, const GatedPlan &g, int smem, cudaStream_t st,
+                        const char *what) {
+  if (ssm_status s = ensure_smem<Kernel>(smem, what)) return s;
+  if (b > kMaxGrid / ((int64_t)g.ctiles * g.csize))
+    return fail(SSM_ERR_UNSUPPORTED, "%s: b * d_in too large for one grid", what);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(b * g.ctiles * g.csize));
+  cfg.blockDim = dim3(ssm::kGatedThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)g.csize;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, Kernel, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(SSM_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
+  }
+  return ok();
+}
+
+template <typename T, bool ASYNC, bool GATE>
+ssm_status gated_fwd_t(ssm::GatedParams p, cudaStream_t st) {
+  const GatedPlan g = gated_plan(p.b, p.L, p.d, 32 * ssm::gated_vec<T>());
+  p.ctiles = g.ctiles, p.csize = g.csize;
+  constexpr int smem = ssm::gated_smem(GATE ? 4 : 3);
+  if (p.start)
+    return launch_gated<ssm::gated_fwd_kernel<T, ASYNC, GATE, true>>(p, p.b, g, smem, st, "ssm_gated_scan_fwd");
+  return launch_gated<ssm::gated_fwd_kernel<T, ASYNC, GATE, false>>(p, p.b, g, smem, st, "ssm_gated_scan_fwd");
+}
+template <typename T, bool ASYNC, bool GATE>
+ssm_status gated_bwd_t(ssm::GatedBwdParams q, int64_t *parts, cudaStream_t st) {
+  const GatedPlan g = gated_plan(q.f.b, q.f.L, q.f.d, 32 * ssm::gated_vec<T>());
+  q.f.ctiles = g.ctiles, q.f.csize = g.csize;
+  *parts = q.f.b * g.csize;
+  constexpr int smem = ssm::gated_smem(GATE ? 5 : 4);
+  if (q.f.start)
+    return launch_gated<ssm::gated_bwd_kernel<T, ASYNC, GATE, true>>(q, q.f.b, g, smem, st, "ssm_gated_scan_bwd");
+  return launch_gated<ssm::gated_bwd_kernel<T, ASYNC, GATE, false>>(q, q.f.b, g, smem, st, "ssm_gated_scan_bwd");
+}
+// Rows in 16-byte pieces (inputs) and VEC elements (outputs) where all allow it.
+template <typename T> ssm_status gated_fwd_any(const ssm::GatedParams &p, cudaStream_t st) {
+  const bool v = vec_rows(16 / sizeof(T), sizeof(T), p.d,
+                          {{p.u, p.u_ld}, {p.ga, p.ga_ld}, {p.gx, p.gx_ld}, {p.z, p.z_ld}}) &&
+                 vec_rows(ssm::gated_vec<T>(), sizeof(T), p.d, {{p.y, p.y_ld}});
+  if (p.z) return v ? gated_fwd_t<T, true, true>(p, st) : gated_fwd_t<T, false, true>(p, st);
+  return v ? gated_fwd_t<T, true, false>(p, st) : gated_fwd_t<T, false, false>(p, st);
+}
+template <typename T>
+ssm_status gated_bwd_any(const ssm::GatedBwdParams &q, int64_t *parts, cudaStream_t st) {
+  const ssm::GatedParams &p = q.f;
+  const bool v = vec_rows(16 / sizeof(T), sizeof(T), p.d,
+                          {{p.u, p.u_ld}, {p.ga, p.ga_ld}, {p.gx, p.gx_ld}, {p.z, p.z_ld},
+                           {q.dout, q.dout_ld}}) &&
+                 vec_rows(ssm::gated_vec<T>(), sizeof(T), p.d,
+                          {{q.du, q.du_ld}, {q.dga, q.dga_ld}, {q.dgx, q.dgx_ld}, {q.dz, q.dz_ld}});
+  if (p.z) return v ? gated_bwd_t<T, true, true>(q, parts, st) : gated_bwd_t<T, false, true>(q, parts, st);
+  return v ? gated_bwd_t<T, true, false>(q, parts, st) : gated_bwd_t<T, false, false>(q, parts, st);
+}
+template <typename T, int VEC>
+ssm_status gated_step_v(const ssm::GatedParams &p, float *state, cudaStream_t st) {
+  const int64_t blocks = (p.b * (p.d / VEC) + 255) / 256;
+  if (blocks > kMaxGrid)
+    return fail(SSM_ERR_UNSUPPORTED, "ssm_gated_state_update: b * d_in too large for one grid");
+  if (p.z)
+    ssm::gated_step_kernel<T, VEC, true><<<(unsigned)blocks, 256, 0, st>>>(p, state);
+  else
+    ssm::gated_step_kernel<T, VEC, false><<<(unsigned)blocks, 256, 0, st>>>(p, state);
+  return check_launch("ssm_gated_state_update");
+}
+template <typename T>
+ssm_status gated_step_any(const ssm::GatedParams &p, float *state, cudaStream_t st) {
+  if (vec_rows(4, sizeof(T), p.d, {{p.u, p.u_ld}, {p.ga, p.ga_ld}, {p.gx, p.gx_ld}, {p.z, p.z_ld},
+                                   {p.y, p.y_ld}}) && aligned(state, 16))
+    return gated_step_v<T, 4>(p, state, st);
+  return gated_step_v<T, 1>(p, state, st);
+}
 
 ssm_status check_gated(const char *what, Args &a, const ssm::GatedParams &p, ssm_dtype dtype) {
   if (ssm_status s = bad_dtype(what, dtype)) return s;
@@ -190,14 +304,6 @@ ssm_status check_states(const char *what, const void *p, size_t have, int64_t b,
 }
 
 // -------------------------------------------------------------- convolution
-// Whether rows of T can be read VEC elements at a time.
-bool vec_rows(int64_t vec, size_t es, int64_t d, std::initializer_list<std::pair<const void *, int64_t>> rows) {
-  if (d % vec != 0) return false;
-  for (const auto &r : rows)
-    if (r.first && (!aligned(r.first, vec * es) || r.second % vec != 0)) return false;
-  return true;
-}
-
 // Shape of the convolution's CTAs: `lanes` channel groups of VEC that fit a
 // warp, 256 / lanes segments of T steps.  A CTA's time goes as T plus the rows a
 // segment reads of its neighbours and its prologue (some 16 rows' worth), so T is
@@ -244,8 +350,6 @@ int64_t conv_bwd_parts(int64_t b, int64_t L, int64_t d) {  // of whichever kerne
     }
   return most;
 }
-
-constexpr int64_t kMaxGrid = 0x7fffffff;
 
 template <typename T, int K, int VEC>
 ssm_status launch_conv_fwd(ssm::ConvParams p, cudaStream_t st) {
@@ -430,11 +534,8 @@ ssm_status ssm_gated_scan_fwd(const void *u, int64_t u_ld, const void *gate_a, i
     if (ssm_status s = check_states(what, chunk_states, chunk_states_bytes, b, L, d_in)) return s;
   if (b == 0 || d_in == 0) return ok();
   if (L == 0) return pass_state(h0, h_last, b * d_in, cu(stream), what);
-  if (dtype == SSM_BF16)
-    ssm::gated_fwd_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p);
-  else
-    ssm::gated_fwd_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p);
-  return check_launch(what);
+  return dtype == SSM_BF16 ? gated_fwd_any<__nv_bfloat16>(p, cu(stream))
+                           : gated_fwd_any<float>(p, cu(stream));
 }
 
 size_t ssm_gated_scan_bwd_workspace_bytes(int64_t b, int64_t L, int64_t d_in) {
@@ -493,12 +594,11 @@ ssm_status ssm_gated_scan_bwd(const void *u, int64_t u_ld, const void *gate_a, i
   float *part = static_cast<float *>(workspace);
   ssm::GatedBwdParams q{f,  dout,  dout_ld, dh_last,    du,         dgate_a, dgate_x,
                         dz, du_ld, dgate_a_ld, dgate_x_ld, dz_ld, dh0, part};
-  if (dtype == SSM_BF16)
-    ssm::gated_bwd_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, st>>>(q);
-  else
-    ssm::gated_bwd_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, st>>>(q);
-  if (ssm_status s = check_launch(what)) return s;
-  return col_sum(part, gated_bwd_parts(b, L, d_in), d_in, dA, d_in, dbias_a, d_in, dbias_x, st, what);
+  int64_t parts = 0;
+  if (ssm_status s = dtype == SSM_BF16 ? gated_bwd_any<__nv_bfloat16>(q, &parts, st)
+                                       : gated_bwd_any<float>(q, &parts, st))
+    return s;
+  return col_sum(part, parts, d_in, dA, d_in, dbias_a, d_in, dbias_x, st, what);
 }
 
 ssm_status ssm_gated_state_update(float *state, const void *u, int64_t u_ld, const void *gate_a,
@@ -518,11 +618,8 @@ ssm_status ssm_gated_state_update(float *state, const void *u, int64_t u_ld, con
   a.rows(true, "y", y, b, d_in, y_ld);
   if (ssm_status s = a.check()) return s;
   if (b == 0 || d_in == 0) return ok();
-  if (dtype == SSM_BF16)
-    ssm::gated_step_kernel<__nv_bfloat16><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p, state);
-  else
-    ssm::gated_step_kernel<float><<<blocks_of(b * d_in, 128), 128, 0, cu(stream)>>>(p, state);
-  return check_launch(what);
+  return dtype == SSM_BF16 ? gated_step_any<__nv_bfloat16>(p, state, cu(stream))
+                           : gated_step_any<float>(p, state, cu(stream));
 }
 
 ssm_status ssm_conv1d_fwd(const void *x, int64_t x_ld, const float *weight, const float *bias,

@@ -3,9 +3,17 @@
 #pragma once
 
 #include "block_common.cuh"
-#include "gated_scan.cuh"
 
 namespace ssm {
+
+template <typename T>
+__device__ __forceinline__ float act_load(const void *p, int64_t i, int64_t n) {
+  return in_bounds(i, n, kBndAct) ? Elem<T>::load(static_cast<const T *>(p), i) : 0.0f;
+}
+template <typename T>
+__device__ __forceinline__ void act_store(void *p, int64_t i, int64_t n, float v) {
+  if (in_bounds(i, n, kBndAct)) Elem<T>::store(static_cast<T *>(p), i, v);
+}
 
 struct GatedNormParams {
   const void *x, *z;
