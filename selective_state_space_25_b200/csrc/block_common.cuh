@@ -42,13 +42,15 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 
 __device__ __forceinline__ float2 f2(float v) { return make_float2(v, v); }
 
-// Decays of two elements from x = A r log2(e): a = 2^x and w = 1 - a^2, both
-// with the accuracy the recurrence needs.  x = j + s with j = rint(x); for
-// j = 0 a - 1 is the polynomial itself, below it a <= 2^-1/2 and a - 1 loses
-// nothing.  w = -(a - 1)(a + 1), at least 0.
+// Decays of two elements from x = A r log2(e), at most 126: a = 2^x and w = 1 -
+// a^2 (or kDecayMinW where that is larger), both with the accuracy the recurrence
+// needs.  x = j + s with j = rint(x), S = 2^j: a = S + S p, a - 1 = S p + (S - 1)
+// with p = 2^s - 1 the polynomial; for j = 0 that is p itself, below it S - 1 is
+// exact and no smaller than 1/2.  w = -(a - 1)(a + 1).
+constexpr float kDecayMinW = 1e-36f;  // its root stands under 1 / f
 __device__ __forceinline__ void decay2(float2 x, float2 &a, float2 &w) {
-  x.x = min_nan(max_nan(x.x, -126.0f), 126.0f);
-  x.y = min_nan(max_nan(x.y, -126.0f), 126.0f);
+  x.x = max_nan(x.x, -126.0f);
+  x.y = max_nan(x.y, -126.0f);
   const float2 t = __fadd2_rn(x, f2(12582912.0f));  // 1.5 2^23: the low bits hold rint(x)
   const float2 j = __fadd2_rn(t, f2(-12582912.0f));
   const float2 s = __ffma2_rn(j, f2(-1.0f), x);     // x - j, exact
@@ -57,18 +59,14 @@ __device__ __forceinline__ void decay2(float2 x, float2 &a, float2 &w) {
   q = __ffma2_rn(q, s, f2(kDecayQ2));
   q = __ffma2_rn(q, s, f2(kDecayQ1));
   q = __ffma2_rn(q, s, f2(kDecayQ0));
-  float2 m = __fmul2_rn(q, s);
-  a = __fadd2_rn(m, f2(1.0f));
-  a.x = __int_as_float(__float_as_int(a.x) + (__float_as_int(t.x) << 23));
-  a.y = __int_as_float(__float_as_int(a.y) + (__float_as_int(t.y) << 23));
-  const float2 m1 = __fadd2_rn(a, f2(-1.0f));
-  m.x = j.x == 0.0f ? m.x : m1.x;
-  m.y = j.y == 0.0f ? m.y : m1.y;
-  // -m (2 + m)
-  const float2 n = __ffma2_rn(m, f2(-1.0f), f2(-2.0f));
-  w = __fmul2_rn(m, n);
-  w.x = max_nan(w.x, 0.0f);
-  w.y = max_nan(w.y, 0.0f);
+  const float2 p = __fmul2_rn(q, s);
+  const float2 S = make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
+                               __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000));
+  a = __ffma2_rn(S, p, S);
+  const float2 m = __ffma2_rn(S, p, __fadd2_rn(S, f2(-1.0f)));
+  w = __fmul2_rn(m, __ffma2_rn(m, f2(-1.0f), f2(-2.0f)));
+  w.x = max_nan(w.x, kDecayMinW);
+  w.y = max_nan(w.y, kDecayMinW);
 }
 
 // ------------------------------------------------------- element access
@@ -147,6 +145,37 @@ __device__ __forceinline__ void st_vec(void *p, int64_t i, int64_t n, const floa
                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
 }
+// Arithmetic on one value or a packed pair (two to an instruction: the same rate a
+// lane, half the issue slots).
+__device__ __forceinline__ float mulv(float a, float b) { return a * b; }
+__device__ __forceinline__ float addv(float a, float b) { return a + b; }
+__device__ __forceinline__ float fmav(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 mulv(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 addv(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fmav(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mulv(float2 a, float b) { return __fmul2_rn(a, f2(b)); }
+__device__ __forceinline__ float ex2v(float x) { return ex2_approx(x); }
+__device__ __forceinline__ float2 ex2v(float2 x) { return make_float2(ex2_approx(x.x), ex2_approx(x.y)); }
+__device__ __forceinline__ float rcpv(float x) { return rcp_approx(x); }
+__device__ __forceinline__ float2 rcpv(float2 x) { return make_float2(rcp_approx(x.x), rcp_approx(x.y)); }
+template <typename F> __device__ __forceinline__ F bc(float v);
+template <> __device__ __forceinline__ float bc<float>(float v) { return v; }
+template <> __device__ __forceinline__ float2 bc<float2>(float v) { return f2(v); }
+__device__ __forceinline__ float hsum(float v) { return v; }
+__device__ __forceinline__ float hsum(float2 v) { return v.x + v.y; }
+template <typename F> __device__ __forceinline__ F sigmoidv(F x) {
+  return rcpv(addv(ex2v(mulv(x, bc<F>(-kLog2e))), bc<F>(1.0f)));
+}
+// E values as pairs where E allows.
+template <int E> struct Lanes {
+  using F = float2;
+  static constexpr int N = E / 2;
+};
+template <> struct Lanes<1> {
+  using F = float;
+  static constexpr int N = 1;
+};
+
 // acc += a * b over VEC values, two to an instruction (packed fp32: the same
 // rate a lane, half the issue slots).
 template <int VEC>

@@ -445,9 +445,217 @@ ssm_status check_conv(const char *what, Args &a, const ssm::ConvParams &p, int64
 }
 
 // -------------------------------------------------------------------- norms
-int64_t norm_bwd_parts(int64_t rows) {
-  const int64_t most = 4 * device_sms();
+// Threads of a row of nv vectors and vectors of a thread (1 .. 4): the pair with
+// the fewest idle places, of those the one with the most vectors a thread, whose
+// loads are in flight together (bf16, 16384 x 1536, forward: 3 a thread 31 us, 2
+// 38, 1 49; backward 80, 84, 128).  Where all rows together do not fill the device,
+// the fewest vectors a thread instead (64 rows: 2.6 us against 3.5).  tpr = 0: longer
+// than 512 threads of 4 vectors hold.
+struct NormPlan {
+  int tpr = 0, vpt = 0, threads = 0;
+};
+NormPlan norm_plan(int64_t rows, int64_t nv) {
+  NormPlan best;
+  int64_t least = -1;
+  const bool few = rows * nv < 512 * (int64_t)device_sms();
+  for (int tpr = 8; tpr <= ssm::kNormMaxTpr; tpr *= 2)
+    for (int vpt = 1; vpt <= 4; ++vpt) {
+      const int64_t idle = (int64_t)tpr * vpt - nv;
+      if (idle < 0) continue;
+      const int64_t cost = few ? vpt * (int64_t)65536 + tpr : idle;
+      if (least < 0 || cost < least) {
+        least = cost;
+        best.tpr = tpr;
+        best.vpt = vpt;
+      }
+    }
+  best.threads = best.tpr > ssm::kNormThreads ? best.tpr : ssm::kNormThreads;
+  return best;
+}
+// CTAs of `threads` threads that an SM holds of a kernel, at most four: the
+// backward runs in one wave of them, each with a partial row of the parameters'
+// gradients (per group).
+constexpr int kNormMaxCtas = 4;
+template <auto Kernel> int norm_ctas(int threads, int smem) {
+  static int cached[64][3] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  int &c = cached[dev][threads <= 256 ? 0 : 1];
+  if (!c) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, threads, (size_t)smem) != cudaSuccess) {
+      cudaGetLastError();
+      n = 1;
+    }
+    c = n < 1 ? 1 : n > kNormMaxCtas ? kNormMaxCtas : n;
+  }
+  return c;
+}
+int64_t norm_parts(int64_t rows, int64_t groups, const NormPlan &n, int ctas) {
+  const int64_t slots = n.threads / n.tpr;
+  int64_t parts = ctas * (int64_t)device_sms() / groups;
+  if (parts < 1) parts = 1;
+  const int64_t rounds = (rows + parts * slots - 1) / (parts * slots);  // rows a slot takes
+  return (rows + rounds * slots - 1) / (rounds * slots);
+}
+int64_t norm_bwd_parts(int64_t rows) {  // of whichever kernel
+  const int64_t most = kNormMaxCtas * (int64_t)device_sms();
   return rows < most ? rows : most;
+}
+
+// Dynamic shared memory of a backward CTA: its slots' columns, summed at its end.
+int norm_smem(const NormPlan &n, int64_t width) {
+  const int64_t slots = n.threads / n.tpr;
+  return slots > 1 ? (int)(slots * width * 4) : 0;
+}
+
+// f(integral_constant<int, vpt>) for 1 <= vpt <= MOST
+template <int MOST, typename F> ssm_status by_vpt(int vpt, F &&f) {
+  if constexpr (MOST > 1)
+    if (vpt < MOST) return by_vpt<MOST - 1>(vpt, f);
+  return f(std::integral_constant<int, MOST>());
+}
+
+template <typename T, int E, int FORM>
+ssm_status gated_norm_fwd_e(ssm::GatedNormParams p, cudaStream_t st) {
+  const char *what = "ssm_gated_norm_fwd";
+  const int64_t rows = p.rows * p.groups;
+  const NormPlan n = norm_plan(rows, p.d / p.groups / E);
+  if (n.tpr == 0) {
+    const unsigned grid = (unsigned)(rows < (1 << 20) ? rows : (1 << 20));
+    ssm::gated_norm_fwd_long_kernel<T><<<grid, ssm::kNormThreads, 0, st>>>(p);
+    return check_launch(what);
+  }
+  p.tpr = n.tpr;
+  const int64_t slots = n.threads / n.tpr, blocks = (rows + slots - 1) / slots;
+  if (blocks > kMaxGrid) return fail(SSM_ERR_UNSUPPORTED, "%s: too many rows for one grid", what);
+  return by_vpt<4>(n.vpt, [&](auto vpt) {
+    ssm::gated_norm_fwd_kernel<T, E, decltype(vpt)::value, FORM><<<(unsigned)blocks, n.threads, 0, st>>>(p);
+    return check_launch(what);
+  });
+}
+template <typename T, int E> ssm_status gated_norm_fwd_f(const ssm::GatedNormParams &p, cudaStream_t st) {
+  if (!p.z) return gated_norm_fwd_e<T, E, ssm::kNoGate>(p, st);
+  return p.before ? gated_norm_fwd_e<T, E, ssm::kNormFirst>(p, st)
+                  : gated_norm_fwd_e<T, E, ssm::kGateFirst>(p, st);
+}
+template <typename T> ssm_status gated_norm_fwd_any(const ssm::GatedNormParams &p, cudaStream_t st) {
+  constexpr int E = 16 / sizeof(T);
+  if (vec_rows(E, sizeof(T), p.d / p.groups, {{p.x, p.x_ld}, {p.z, p.z_ld}, {p.y, p.y_ld}}) &&
+      aligned(p.w, 16))
+    return gated_norm_fwd_f<T, E>(p, st);
+  return gated_norm_fwd_f<T, 1>(p, st);
+}
+
+template <typename T, int E, int FORM>
+ssm_status gated_norm_bwd_e(ssm::GatedNormBwdParams q, int64_t *parts, cudaStream_t st) {
+  const char *what = "ssm_gated_norm_bwd";
+  ssm::GatedNormParams &p = q.f;
+  const NormPlan n = norm_plan(p.rows * p.groups, p.d / p.groups / E);
+  if (n.tpr == 0) {
+    *parts = norm_bwd_parts(p.rows);
+    ssm::gated_norm_bwd_long_kernel<T><<<(unsigned)*parts, ssm::kNormThreads, 0, st>>>(q);
+    return check_launch(what);
+  }
+  p.tpr = n.tpr;
+  const int smem = norm_smem(n, p.d / p.groups);
+  return by_vpt<4>(n.vpt, [&](auto vpt) {
+    constexpr auto kernel = ssm::gated_norm_bwd_kernel<T, E, decltype(vpt)::value, FORM>;
+    *parts = norm_parts(p.rows, p.groups, n, norm_ctas<kernel>(n.threads, smem));
+    q.parts = (int)*parts;
+    if (*parts > kMaxGrid / p.groups) return fail(SSM_ERR_UNSUPPORTED, "%s: too many groups", what);
+    kernel<<<(unsigned)(*parts * p.groups), n.threads, smem, st>>>(q);
+    return check_launch(what);
+  });
+}
+template <typename T, int E>
+ssm_status gated_norm_bwd_f(const ssm::GatedNormBwdParams &q, int64_t *parts, cudaStream_t st) {
+  if (!q.f.z) return gated_norm_bwd_e<T, E, ssm::kNoGate>(q, parts, st);
+  return q.f.before ? gated_norm_bwd_e<T, E, ssm::kNormFirst>(q, parts, st)
+                    : gated_norm_bwd_e<T, E, ssm::kGateFirst>(q, parts, st);
+}
+template <typename T>
+ssm_status gated_norm_bwd_any(const ssm::GatedNormBwdParams &q, int64_t *parts, cudaStream_t st) {
+  constexpr int E = ssm::kNormBwdElems;
+  const ssm::GatedNormParams &p = q.f;
+  if (vec_rows(E, sizeof(T), p.d / p.groups,
+               {{p.x, p.x_ld}, {p.z, p.z_ld}, {q.dy, q.dy_ld}, {q.dx, q.dx_ld}, {q.dz, q.dz_ld}}) &&
+      aligned(p.w, 16))
+    return gated_norm_bwd_f<T, E>(q, parts, st);
+  return gated_norm_bwd_f<T, 1>(q, parts, st);
+}
+
+bool add_norm_vec(int64_t E, size_t es, size_t rs, const ssm::AddNormParams &p,
+                  std::initializer_list<std::pair<const void *, int64_t>> act,
+                  std::initializer_list<std::pair<const void *, int64_t>> res) {
+  if (!vec_rows(E, es, p.d, act) || !aligned(p.w, 16)) return false;
+  if (p.d % E != 0 || (p.post && !aligned(p.post, 16)) || (p.scale && !aligned(p.scale, 16))) return false;
+  for (const auto &r : res) {  // at most 16 bytes an access
+    const size_t a = E * rs < 16 ? E * rs : 16;
+    if (r.first && (!aligned(r.first, a) || r.second * rs % a != 0)) return false;
+  }
+  return true;
+}
+
+template <typename T, typename R, int E>
+ssm_status add_norm_fwd_e(ssm::AddNormParams p, cudaStream_t st) {
+  const char *what = "ssm_add_norm_fwd";
+  const NormPlan n = norm_plan(p.rows, p.d / E);
+  if (n.tpr == 0) {
+    const unsigned grid = (unsigned)(p.rows < (1 << 20) ? p.rows : (1 << 20));
+    ssm::add_norm_fwd_long_kernel<T, R><<<grid, ssm::kNormThreads, 0, st>>>(p);
+    return check_launch(what);
+  }
+  p.tpr = n.tpr;
+  const int64_t slots = n.threads / n.tpr, blocks = (p.rows + slots - 1) / slots;
+  if (blocks > kMaxGrid) return fail(SSM_ERR_UNSUPPORTED, "%s: too many rows for one grid", what);
+  return by_vpt<4>(n.vpt, [&](auto vpt) {
+    ssm::add_norm_fwd_kernel<T, R, E, decltype(vpt)::value><<<(unsigned)blocks, n.threads, 0, st>>>(p);
+    return check_launch(what);
+  });
+}
+template <typename T, typename R> ssm_status add_norm_fwd_any(const ssm::AddNormParams &p, cudaStream_t st) {
+  constexpr int E = 16 / sizeof(T);
+  if (add_norm_vec(E, sizeof(T), sizeof(R), p, {{p.x, p.x_ld}, {p.y, p.y_ld}},
+                   {{p.res, p.res_ld}, {p.res_out, p.ro_ld}}))
+    return add_norm_fwd_e<T, R, E>(p, st);
+  return add_norm_fwd_e<T, R, 1>(p, st);
+}
+
+template <typename T, typename R, int E, bool POST, bool SCALE>
+ssm_status add_norm_bwd_f(ssm::AddNormBwdParams q, int64_t *parts, cudaStream_t st) {
+  const char *what = "ssm_add_norm_bwd";
+  const NormPlan n = norm_plan(q.f.rows, q.f.d / E);
+  if (n.tpr == 0) {
+    *parts = norm_bwd_parts(q.f.rows);
+    ssm::add_norm_bwd_long_kernel<T, R><<<(unsigned)*parts, ssm::kNormThreads, 0, st>>>(q);
+    return check_launch(what);
+  }
+  q.f.tpr = n.tpr;
+  const int smem = norm_smem(n, q.f.d);
+  return by_vpt<4>(n.vpt, [&](auto vpt) {
+    constexpr auto kernel = ssm::add_norm_bwd_kernel<T, R, E, decltype(vpt)::value, POST, SCALE>;
+    *parts = norm_parts(q.f.rows, 1, n, norm_ctas<kernel>(n.threads, smem));
+    q.parts = (int)*parts;
+    kernel<<<(unsigned)*parts, n.threads, smem, st>>>(q);
+    return check_launch(what);
+  });
+}
+template <typename T, typename R, int E>
+ssm_status add_norm_bwd_e(const ssm::AddNormBwdParams &q, int64_t *parts, cudaStream_t st) {
+  if (q.f.post)
+    return q.f.scale ? add_norm_bwd_f<T, R, E, true, true>(q, parts, st)
+                     : add_norm_bwd_f<T, R, E, true, false>(q, parts, st);
+  return q.f.scale ? add_norm_bwd_f<T, R, E, false, true>(q, parts, st)
+                   : add_norm_bwd_f<T, R, E, false, false>(q, parts, st);
+}
+template <typename T, typename R>
+ssm_status add_norm_bwd_any(const ssm::AddNormBwdParams &q, int64_t *parts, cudaStream_t st) {
+  constexpr int E = ssm::kNormBwdElems;
+  if (add_norm_vec(E, sizeof(T), sizeof(R), q.f, {{q.f.x, q.f.x_ld}, {q.dy, q.dy_ld}, {q.dx, q.dx_ld}},
+                   {{q.f.res_out, q.f.ro_ld}, {q.dro, q.dro_ld}, {q.dres, q.dres_ld}}))
+    return add_norm_bwd_e<T, R, E>(q, parts, st);
+  return add_norm_bwd_e<T, R, 1>(q, parts, st);
 }
 
 ssm_status check_eps(const char *what, float eps) {
@@ -725,13 +933,8 @@ ssm_status ssm_gated_norm_fwd(const void *x, int64_t x_ld, const void *z, int64_
   a.rows(true, "y", y, rows, d, y_ld);
   if (ssm_status s = a.check()) return s;
   if (rows == 0 || d == 0) return ok();
-  const int64_t n = rows * groups;
-  const unsigned grid = (unsigned)(n < (1 << 20) ? n : (1 << 20));
-  if (dtype == SSM_BF16)
-    ssm::gated_norm_fwd_kernel<__nv_bfloat16><<<grid, ssm::kNormThreads, 0, cu(stream)>>>(p);
-  else
-    ssm::gated_norm_fwd_kernel<float><<<grid, ssm::kNormThreads, 0, cu(stream)>>>(p);
-  return check_launch(what);
+  return dtype == SSM_BF16 ? gated_norm_fwd_any<__nv_bfloat16>(p, cu(stream))
+                           : gated_norm_fwd_any<float>(p, cu(stream));
 }
 
 size_t ssm_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t d, int64_t groups) {
@@ -766,13 +969,11 @@ ssm_status ssm_gated_norm_bwd(const void *x, int64_t x_ld, const void *z, int64_
   if (rows == 0) return zero(dweight, d, st, what);
   if (ssm_status s = need_workspace(what, workspace, workspace_bytes, need)) return s;
   float *part = static_cast<float *>(workspace);
-  const int64_t n = norm_bwd_parts(rows);
-  ssm::GatedNormBwdParams q{p, dy, dy_ld, dx, dz, dx_ld, dz_ld, part};
-  if (dtype == SSM_BF16)
-    ssm::gated_norm_bwd_kernel<__nv_bfloat16><<<(unsigned)n, ssm::kNormThreads, 0, st>>>(q);
-  else
-    ssm::gated_norm_bwd_kernel<float><<<(unsigned)n, ssm::kNormThreads, 0, st>>>(q);
-  if (ssm_status s = check_launch(what)) return s;
+  ssm::GatedNormBwdParams q{p, dy, dy_ld, dx, dz, dx_ld, dz_ld, 0, part};
+  int64_t n = 0;
+  if (ssm_status s = dtype == SSM_BF16 ? gated_norm_bwd_any<__nv_bfloat16>(q, &n, st)
+                                       : gated_norm_bwd_any<float>(q, &n, st))
+    return s;
   return col_sum(part, n, d, dweight, 0, nullptr, 0, nullptr, st, what);
 }
 
@@ -795,15 +996,10 @@ ssm_status ssm_add_norm_fwd(const void *x, int64_t x_ld, const void *residual, i
   a.same("residual_out", "residual");
   if (ssm_status s = a.check()) return s;
   if (rows == 0 || d == 0) return ok();
-  const unsigned grid = (unsigned)(rows < (1 << 20) ? rows : (1 << 20));
   using bf16 = __nv_bfloat16;
-  if (dtype == SSM_F32)
-    ssm::add_norm_fwd_kernel<float, float><<<grid, ssm::kNormThreads, 0, cu(stream)>>>(p);
-  else if (residual_dtype == SSM_F32)
-    ssm::add_norm_fwd_kernel<bf16, float><<<grid, ssm::kNormThreads, 0, cu(stream)>>>(p);
-  else
-    ssm::add_norm_fwd_kernel<bf16, bf16><<<grid, ssm::kNormThreads, 0, cu(stream)>>>(p);
-  return check_launch(what);
+  if (dtype == SSM_F32) return add_norm_fwd_any<float, float>(p, cu(stream));
+  return residual_dtype == SSM_F32 ? add_norm_fwd_any<bf16, float>(p, cu(stream))
+                                   : add_norm_fwd_any<bf16, bf16>(p, cu(stream));
 }
 
 size_t ssm_add_norm_bwd_workspace_bytes(int64_t rows, int64_t d) {
@@ -855,17 +1051,14 @@ ssm_status ssm_add_norm_bwd(const void *x, int64_t x_ld, const void *residual_ou
   }
   if (ssm_status s = need_workspace(what, workspace, workspace_bytes, need)) return s;
   float *part = static_cast<float *>(workspace);
-  const int64_t n = norm_bwd_parts(rows);
   ssm::AddNormBwdParams q{p, dy, dresidual_out, dy_ld, dresidual_out_ld, dx, dresidual, dx_ld,
-                          dresidual_ld, part};
+                          dresidual_ld, 0, part};
   using bf16 = __nv_bfloat16;
-  if (dtype == SSM_F32)
-    ssm::add_norm_bwd_kernel<float, float><<<(unsigned)n, ssm::kNormThreads, 0, st>>>(q);
-  else if (residual_dtype == SSM_F32)
-    ssm::add_norm_bwd_kernel<bf16, float><<<(unsigned)n, ssm::kNormThreads, 0, st>>>(q);
-  else
-    ssm::add_norm_bwd_kernel<bf16, bf16><<<(unsigned)n, ssm::kNormThreads, 0, st>>>(q);
-  if (ssm_status s = check_launch(what)) return s;
+  int64_t n = 0;
+  if (ssm_status s = dtype == SSM_F32            ? add_norm_bwd_any<float, float>(q, &n, st)
+                     : residual_dtype == SSM_F32 ? add_norm_bwd_any<bf16, float>(q, &n, st)
+                                                 : add_norm_bwd_any<bf16, bf16>(q, &n, st))
+    return s;
   return col_sum(part, n, d, dweight, d, dpost_weight, d, dscale, st, what);
 }
 

@@ -98,10 +98,6 @@ __device__ __forceinline__ float2 silu_2(float2 z) {
   return mul2(z, s);
 }
 
-// 1 - a^2 at least this: its root stands under 1 / f and in products with
-// (1 + e^-x)^2; f = 0 becomes 1e-18.
-constexpr float kGatedMinW = 1e-36f;
-
 // Composition: state after the map (P, Q) from state h.  With START a P of 0
 // says that a sequence started on the way: nothing of h remains, NaN neither.
 template <bool START> __device__ __forceinline__ float through(float P, float h, float Q) {
@@ -112,6 +108,34 @@ template <bool START> __device__ __forceinline__ float through(float P, float h,
 template <bool START> __device__ __forceinline__ float times(float P, float a) {
   const float r = P * a;
   return START && (P == 0.0f || a == 0.0f) ? 0.0f : r;
+}
+
+// m after `front`, both (P, P, Q, Q) of a lane's channels.
+template <int VEC, bool START> __device__ __forceinline__ void gated_compose(float4 &front, float4 m) {
+  front.z = through<START>(m.x, front.z, m.z);
+  front.x = times<START>(front.x, m.x);
+  if constexpr (VEC == 2) {
+    front.w = through<START>(m.y, front.w, m.w);
+    front.y = times<START>(front.y, m.y);
+  }
+}
+
+// Makes the tiles' compositions, which one warp of each CTA wrote, known to all
+// of the cluster.  Only that warp releases at cluster scope (a release waits for
+// a warp's global stores too): its release covers what the CTA's other warps
+// read of the buffer two rounds ago, which the round's __syncthreads ordered
+// before it.
+__device__ __forceinline__ void gated_exchange(int C, bool writer) {
+  if (C == 1) {
+    __syncthreads();
+    return;
+  }
+  __syncwarp();
+  if (writer)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  else
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  cluster_wait();
 }
 
 // Per-lane constants: VEC channels from c0 (the pair's two for VEC = 2, one
@@ -134,44 +158,71 @@ template <int VEC>
 __device__ __forceinline__ GatedLane gated_lane(const GatedParams &p, int64_t c) {
   GatedLane l;
   l.A2 = mul2(lane_pair<VEC>(p.A, c, p.d), f2(kLog2e));
+  l.A2 = make_float2(min_nan(l.A2.x, 126.0f), min_nan(l.A2.y, 126.0f));
   l.na = mul2(lane_pair<VEC>(p.ba, c, p.d), f2(-kLog2e));
   l.nx = mul2(lane_pair<VEC>(p.bx, c, p.d), f2(-kLog2e));
   return l;
 }
 
 // ----------------------------------------------------------------- staging
-// Copies a warp's 8 rows of one tensor (rows t .. t + n - 1 of 128 bytes) into its
-// stage, past-the-end rows and channels as zeros.  ASYNC: 16-byte cp.async (rows
-// 16-byte aligned, d a multiple of 16 bytes); else element loads.
-template <typename T, bool ASYNC>
-__device__ __forceinline__ void stage_rows(char *s, const void *src, int64_t ld, int64_t row, int n,
-                                           int64_t c0, int64_t d, int64_t ext, int lane) {
-  constexpr int VEC = gated_vec<T>();
-  const T *base = static_cast<const T *>(src);
-  if constexpr (ASYNC) {
+// One tensor's rows for a warp: 8 rows of 128 bytes a tile, `step` bytes to the
+// next tile's.  ASYNC: 16-byte cp.async (rows 16-byte aligned, d a multiple of 16
+// bytes), lane l the piece l % 8 of rows l / 8 and l / 8 + 4; else element loads.
+// Rows past the end and channels past d become zeros.
+template <typename T, bool ASYNC> struct GatedSrc {
+  const char *p;      // the lane's first element of the next tile
+  int64_t ld, step;   // bytes
+  const char *lo, *hi;  // the buffer (debug-bounds build)
+  __device__ __forceinline__ void init(const void *src, int64_t ld_, int64_t row, int64_t tile_rows,
+                                       int64_t c0, int lane, int64_t rows, int64_t d) {
     constexpr int E = 16 / (int)sizeof(T);
-#pragma unroll
-    for (int j = 0; j < kGatedSteps * kGatedRowBytes / 16 / 32; ++j) {
-      const int k = lane + 32 * j, r = k / 8, q = k % 8;
-      const int64_t c = c0 + q * E, i = (row + r) * ld + c;
-      const bool ok = r < n && c < d && in_bounds(i, ext - (E - 1), kBndAct);
-      cp_async16(s + r * kGatedRowBytes + q * 16, ok ? base + i : base, ok ? 16 : 0);
-    }
-  } else {
-    T v[kGatedSteps][VEC];
-#pragma unroll
-    for (int r = 0; r < kGatedSteps; ++r)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int64_t c = c0 + lane * VEC + e, i = (row + r) * ld + c;
-        v[r][e] = r < n && c < d && in_bounds(i, ext, kBndAct) ? base[i] : T(0.0f);
-      }
-#pragma unroll
-    for (int r = 0; r < kGatedSteps; ++r)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        reinterpret_cast<T *>(s + r * kGatedRowBytes)[lane * VEC + e] = v[r][e];
+    ld = ld_ * (int64_t)sizeof(T);
+    step = tile_rows * ld;
+    lo = static_cast<const char *>(src);
+    hi = lo + extent(rows, d, ld_) * (int64_t)sizeof(T);
+    p = lo + row * ld + c0 * (int64_t)sizeof(T) +
+        (ASYNC ? lane / 8 * ld + lane % 8 * 16 : lane * gated_vec<T>() * (int64_t)sizeof(T));
+    (void)E;
   }
+  // n rows of this tile; bytes: 16 where the lane's piece lies in front of d, else
+  // 0 (elements: how many of the lane's do)
+  __device__ __forceinline__ void fetch(char *s, int n, int bytes, int lane) {
+    if constexpr (ASYNC) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const char *q = p + 4 * j * ld;
+        int b = bytes;
+        if (n < kGatedSteps && lane / 8 + 4 * j >= n) b = 0;
+        if (b && !in_bounds(q - lo, hi - lo - 15, kBndAct)) b = 0;
+        if (n < kGatedSteps && !b) q = lo;
+        cp_async16(s + j * 512 + lane * 16, q, b);
+      }
+    } else {
+      constexpr int VEC = gated_vec<T>();
+      T v[kGatedSteps][VEC];
+#pragma unroll
+      for (int r = 0; r < kGatedSteps; ++r)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const char *q = p + r * ld + e * (int)sizeof(T);
+          v[r][e] = r < n && e < bytes && in_bounds(q - lo, hi - lo, kBndAct)
+                        ? *reinterpret_cast<const T *>(q) : T(0.0f);
+        }
+#pragma unroll
+      for (int r = 0; r < kGatedSteps; ++r)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          reinterpret_cast<T *>(s + r * kGatedRowBytes)[lane * VEC + e] = v[r][e];
+    }
+    p += step;
+  }
+};
+// The `bytes` of fetch for a lane.
+template <typename T, bool ASYNC>
+__device__ __forceinline__ int gated_piece(int64_t c0, int lane, int64_t d) {
+  if constexpr (ASYNC) return c0 + lane % 8 * (16 / (int)sizeof(T)) < d ? 16 : 0;
+  const int64_t left = d - c0 - lane * gated_vec<T>();
+  return left < 0 ? 0 : left < gated_vec<T>() ? (int)left : gated_vec<T>();
 }
 
 // Flat element k of a lane: step k / VEC, channel k % VEC.  Pair k of one staged
@@ -222,9 +273,16 @@ __global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const Gated
   char *mine = stage + warp * NT * kGatedStage;
   constexpr int kHalf = NT * kGatedWarps * kGatedStage;
   const GatedLane k = gated_lane<VEC>(p, c);
-  const int64_t xu = extent(R, p.d, p.u_ld), xa = extent(R, p.d, p.ga_ld),
-                xg = extent(R, p.d, p.gx_ld), xz = extent(R, p.d, p.z_ld),
-                xy = extent(R, p.d, p.y_ld);
+  const int64_t t_first = rank * kGatedChunk + warp * kGatedSteps;  // the warp's first step
+  const int64_t row0 = i * p.L + t_first;
+  const int64_t tile_rows = (int64_t)C * kGatedChunk;
+  GatedSrc<T, ASYNC> su, sa, sg, sz;
+  su.init(p.u, p.u_ld, row0, tile_rows, c0, lane, R, p.d);
+  sa.init(p.ga, p.ga_ld, row0, tile_rows, c0, lane, R, p.d);
+  sg.init(p.gx, p.gx_ld, row0, tile_rows, c0, lane, R, p.d);
+  if constexpr (GATE) sz.init(p.z, p.z_ld, row0, tile_rows, c0, lane, R, p.d);
+  const int piece = gated_piece<T, ASYNC>(c0, lane, p.d);
+  const int64_t xy = extent(R, p.d, p.y_ld);
   float h[VEC];  // state in front of the cluster's next tiles
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
@@ -233,22 +291,23 @@ __global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const Gated
       h[e] = p.h0[i * p.d + c + e];
   }
   unsigned flag = 0;  // lane r: whether a sequence starts at the next tile's row r
-  const auto rows_of = [&](int it, int64_t &row) {  // the warp's rows of the CTA's tile
-    const int64_t t = (it * (int64_t)C + rank) * kGatedChunk + warp * kGatedSteps;
-    row = i * p.L + t;
-    return t < p.L ? (int)(p.L - t < kGatedSteps ? p.L - t : kGatedSteps) : 0;
+  // the warp's rows of its CTA's tile of round `it`
+  const auto rows_of = [&](int it) {
+    const int64_t left = p.L - t_first - it * tile_rows;
+    return left >= kGatedSteps ? kGatedSteps : left > 0 ? (int)left : 0;
   };
   const auto fetch = [&](int it) {
     if (it < iters) {
-      int64_t row;
-      const int n = rows_of(it, row);
+      const int n = rows_of(it);
       char *s = mine + (it & 1) * kHalf;
-      stage_rows<T, ASYNC>(s, p.u, p.u_ld, row, n, c0, p.d, xu, lane);
-      stage_rows<T, ASYNC>(s + kGatedStage, p.ga, p.ga_ld, row, n, c0, p.d, xa, lane);
-      stage_rows<T, ASYNC>(s + 2 * kGatedStage, p.gx, p.gx_ld, row, n, c0, p.d, xg, lane);
-      if constexpr (GATE)
-        stage_rows<T, ASYNC>(s + 3 * kGatedStage, p.z, p.z_ld, row, n, c0, p.d, xz, lane);
-      if (START) flag = lane < n && in_bounds(row + lane, R, kBndAct) ? p.start[row + lane] : 0;
+      su.fetch(s, n, piece, lane);
+      sa.fetch(s + kGatedStage, n, piece, lane);
+      sg.fetch(s + 2 * kGatedStage, n, piece, lane);
+      if constexpr (GATE) sz.fetch(s + 3 * kGatedStage, n, piece, lane);
+      if (START) {
+        const int64_t r = row0 + it * tile_rows + lane;
+        flag = lane < n && in_bounds(r, R, kBndAct) ? p.start[r] : 0;
+      }
     }
     cp_async_commit();
   };
@@ -263,8 +322,7 @@ __global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const Gated
     fetch(it + 1);
     cp_async_wait<1>();
     __syncwarp();
-    int64_t row;
-    const int n = rows_of(it, row);
+    const int n = rows_of(it);
     const char *s = mine + (it & 1) * kHalf;
     // decays and drives of the warp's steps, and their composition
     float a[E], x[E];
@@ -276,13 +334,11 @@ __global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const Gated
       const float2 q1 = __fadd2_rn(eg, f2(1.0f));
       float2 av, w;
       decay2(mul2(k.A2, r), av, w);
-      w.x = max_nan(w.x, kGatedMinW);
-      w.y = max_nan(w.y, kGatedMinW);
       const float2 u = staged_pair<T>(s, q, lane);
       // f g = w / sqrt(w (1 + e^-x)^2)
       const float2 fg = mul2(w, rsqrt_2(mul2(mul2(w, q1), q1)));
       float2 xv = mul2(fg, u);
-      if (START) {
+      if (START && bits) {
         const int s0 = 2 * q / VEC, s1 = (2 * q + 1) / VEC;
         if (bits >> s0 & 1) av.x = 0.0f, xv.x = u.x * rcp_approx(q1.x);
         if (bits >> s1 & 1) av.y = 0.0f, xv.y = u.y * rcp_approx(q1.y);
@@ -290,52 +346,44 @@ __global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const Gated
       a[2 * q] = av.x, a[2 * q + 1] = av.y;
       x[2 * q] = xv.x, x[2 * q + 1] = xv.y;
     }
-    float P[VEC], Q[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) P[e] = 1.0f, Q[e] = 0.0f;
     if (n < kGatedSteps) {  // steps past the end change nothing
 #pragma unroll
       for (int q = 0; q < E; ++q)
         if (q / VEC >= n) a[q] = 1.0f, x[q] = 0.0f;
     }
+    float P[VEC], Q[VEC];
 #pragma unroll
-    for (int q = 0; q < E; ++q) {
+    for (int e = 0; e < VEC; ++e) P[e] = a[e], Q[e] = x[e];
+#pragma unroll
+    for (int q = VEC; q < E; ++q) {
       Q[q % VEC] = through<START>(a[q], Q[q % VEC], x[q]);
       P[q % VEC] = times<START>(P[q % VEC], a[q]);
     }
     const int par = it & 1;
     wsum[par][warp][lane] = make_float4(P[0], P[VEC - 1], Q[0], Q[VEC - 1]);
     __syncthreads();
-    // the tile's composition, and of the steps in front of this warp's
-    float4 front = make_float4(1.0f, 1.0f, 0.0f, 0.0f), all = front;
-#pragma unroll
-    for (int w = 0; w < kGatedWarps; ++w) {
-      if (w == warp) front = all;
-      const float4 m = wsum[par][w][lane];
-      all.z = through<START>(m.x, all.z, m.z);
-      all.w = through<START>(m.y, all.w, m.w);
-      all.x = times<START>(all.x, m.x);
-      all.y = times<START>(all.y, m.y);
+    // composition of the steps in front of this warp's; the last warp's, with its
+    // own, is the tile's
+    float4 front = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+    for (int w = 0; w < warp; ++w) gated_compose<VEC, START>(front, wsum[par][w][lane]);
+    if (warp == kGatedWarps - 1) {
+      float4 all = front;
+      gated_compose<VEC, START>(all, make_float4(P[0], P[VEC - 1], Q[0], Q[VEC - 1]));
+      if (C > 1)
+        for (int w = 0; w < C; ++w) st_peer(&csum[par][rank][lane], w, all);
+      else
+        csum[par][0][lane] = all;
     }
+    gated_exchange(C, warp == kGatedWarps - 1);
     float hs[VEC];  // state in front of the warp's steps
-    if (C > 1) {
-      if (warp < C) st_peer(&csum[par][rank][lane], warp, all);
-      cluster_arrive();
-      cluster_wait();
-      for (int w = 0; w < C; ++w) {
-        if (w == rank) {
+    for (int w = 0; w < C; ++w) {
+      if (w == rank) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) hs[e] = h[e];
-        }
-        const float4 m = csum[par][w][lane];
-        h[0] = through<START>(m.x, h[0], m.z);
-        if constexpr (VEC == 2) h[1] = through<START>(m.y, h[1], m.w);
+        for (int e = 0; e < VEC; ++e) hs[e] = h[e];
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) hs[e] = h[e];
-      h[0] = through<START>(all.x, h[0], all.z);
-      if constexpr (VEC == 2) h[1] = through<START>(all.y, h[1], all.w);
+      const float4 m = csum[par][w][lane];
+      h[0] = through<START>(m.x, h[0], m.z);
+      if constexpr (VEC == 2) h[1] = through<START>(m.y, h[1], m.w);
     }
     const int64_t tile = it * (int64_t)C + rank;
     if (p.chunk_h && warp == 0 && tile < nT) {
@@ -360,9 +408,16 @@ __global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const Gated
         x[2 * q] = o.x, x[2 * q + 1] = o.y;
       }
     }
+    const int64_t row = row0 + it * tile_rows;
+    if (n == kGatedSteps) {
 #pragma unroll
-    for (int t = 0; t < kGatedSteps; ++t)
-      if (t < n) store_step<T, ASYNC>(p.y, p.y_ld, row + t, c, p.d, xy, x + t * VEC);
+      for (int t = 0; t < kGatedSteps; ++t)
+        store_step<T, ASYNC>(p.y, p.y_ld, row + t, c, p.d, xy, x + t * VEC);
+    } else {
+#pragma unroll
+      for (int t = 0; t < kGatedSteps; ++t)
+        if (t < n) store_step<T, ASYNC>(p.y, p.y_ld, row + t, c, p.d, xy, x + t * VEC);
+    }
   }
   if (p.h_last && rank == 0 && warp == 0) {
 #pragma unroll
@@ -396,10 +451,19 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
   char *mine = stage + warp * NT * kGatedStage;
   constexpr int kHalf = NT * kGatedWarps * kGatedStage;
   const GatedLane k = gated_lane<VEC>(p, c);
-  const int64_t xu = extent(R, p.d, p.u_ld), xa = extent(R, p.d, p.ga_ld),
-                xg = extent(R, p.d, p.gx_ld), xz = extent(R, p.d, p.z_ld),
-                xo = extent(R, p.d, q_.dout_ld), yu = extent(R, p.d, q_.du_ld),
-                ya = extent(R, p.d, q_.dga_ld), yg = extent(R, p.d, q_.dgx_ld),
+  // tiles from the end: rank 0 takes the last of the cluster's
+  const int64_t tile0 = nT - 1 - rank;
+  const int64_t t_first = tile0 * kGatedChunk + warp * kGatedSteps;  // the warp's first step
+  const int64_t row0 = i * p.L + t_first;
+  const int64_t tile_rows = -(int64_t)C * kGatedChunk;
+  GatedSrc<T, ASYNC> su, s_a, sg, so, sz;
+  su.init(p.u, p.u_ld, row0, tile_rows, c0, lane, R, p.d);
+  s_a.init(p.ga, p.ga_ld, row0, tile_rows, c0, lane, R, p.d);
+  sg.init(p.gx, p.gx_ld, row0, tile_rows, c0, lane, R, p.d);
+  so.init(q_.dout, q_.dout_ld, row0, tile_rows, c0, lane, R, p.d);
+  if constexpr (GATE) sz.init(p.z, p.z_ld, row0, tile_rows, c0, lane, R, p.d);
+  const int piece = gated_piece<T, ASYNC>(c0, lane, p.d);
+  const int64_t yu = extent(R, p.d, q_.du_ld), ya = extent(R, p.d, q_.dga_ld), yg = extent(R, p.d, q_.dgx_ld),
                 yz = extent(R, p.d, q_.dz_ld);
   float mu[VEC];                          // adjoint behind the cluster's next tiles
   float2 sA = f2(0.0f), sa = sA, sx = sA;  // sums of dl r, dgate_a / A, dgate_x
@@ -413,27 +477,25 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
   float hnext[VEC];  // the next tile's start state
 #pragma unroll
   for (int e = 0; e < VEC; ++e) hnext[e] = 0.0f;
-  // tiles from the end: rank 0 takes the last of the cluster's
-  const auto tile_of = [&](int it) { return nT - 1 - (it * (int64_t)C + rank); };
-  const auto rows_of = [&](int it, int64_t &row) {
-    const int64_t tile = tile_of(it), t = tile * kGatedChunk + warp * kGatedSteps;
-    row = i * p.L + t;
-    if (tile < 0 || t >= p.L) return 0;
-    return (int)(p.L - t < kGatedSteps ? p.L - t : kGatedSteps);
+  const auto rows_of = [&](int it) {
+    if (tile0 - it * (int64_t)C < 0) return 0;
+    const int64_t left = p.L - t_first - it * tile_rows;
+    return left >= kGatedSteps ? kGatedSteps : left > 0 ? (int)left : 0;
   };
   const auto fetch = [&](int it) {
     if (it < iters) {
-      int64_t row;
-      const int n = rows_of(it, row);
+      const int n = rows_of(it);
       char *s = mine + (it & 1) * kHalf;
-      stage_rows<T, ASYNC>(s, p.u, p.u_ld, row, n, c0, p.d, xu, lane);
-      stage_rows<T, ASYNC>(s + kGatedStage, p.ga, p.ga_ld, row, n, c0, p.d, xa, lane);
-      stage_rows<T, ASYNC>(s + 2 * kGatedStage, p.gx, p.gx_ld, row, n, c0, p.d, xg, lane);
-      stage_rows<T, ASYNC>(s + 3 * kGatedStage, q_.dout, q_.dout_ld, row, n, c0, p.d, xo, lane);
-      if constexpr (GATE)
-        stage_rows<T, ASYNC>(s + 4 * kGatedStage, p.z, p.z_ld, row, n, c0, p.d, xz, lane);
-      if (START) flag = lane < n && in_bounds(row + lane, R, kBndAct) ? p.start[row + lane] : 0;
-      const int64_t tile = tile_of(it);
+      su.fetch(s, n, piece, lane);
+      s_a.fetch(s + kGatedStage, n, piece, lane);
+      sg.fetch(s + 2 * kGatedStage, n, piece, lane);
+      so.fetch(s + 3 * kGatedStage, n, piece, lane);
+      if constexpr (GATE) sz.fetch(s + 4 * kGatedStage, n, piece, lane);
+      if (START) {
+        const int64_t r = row0 + it * tile_rows + lane;
+        flag = lane < n && in_bounds(r, R, kBndAct) ? p.start[r] : 0;
+      }
+      const int64_t tile = tile0 - it * (int64_t)C;
       if (tile >= 0) {
         const int64_t o = (i * nT + tile) * p.d + c, on = p.b * nT * p.d;
 #pragma unroll
@@ -457,8 +519,8 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
     fetch(it + 1);
     cp_async_wait<1>();
     __syncwarp();
-    int64_t row;
-    const int n = rows_of(it, row);
+    const int64_t row = row0 + it * tile_rows;
+    const int n = rows_of(it);
     char *s = mine + (it & 1) * kHalf;
     float a[E], f[E], af[E], g[E], lam[E];  // af = a^2 / f; lam: dout silu(z), later the adjoint
 #pragma unroll
@@ -472,11 +534,10 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
       const float2 r = mul2(inv, eg), gv = mul2(inv, er);
       float2 av, w;
       decay2(mul2(k.A2, r), av, w);
-      const float2 wm = make_float2(max_nan(w.x, kGatedMinW), max_nan(w.y, kGatedMinW));
-      float2 rho = rsqrt_2(wm);
-      float2 fv = mul2(wm, rho);
-      rho = make_float2(w.x == 0.0f ? 0.0f : rho.x, w.y == 0.0f ? 0.0f : rho.y);
-      if (START) {
+      float2 rho = rsqrt_2(w);
+      float2 fv = mul2(w, rho);
+      rho = make_float2(w.x == kDecayMinW ? 0.0f : rho.x, w.y == kDecayMinW ? 0.0f : rho.y);
+      if (START && bits) {
         const int s0 = 2 * q / VEC, s1 = (2 * q + 1) / VEC;
         if (bits >> s0 & 1) av.x = 0.0f, fv.x = 1.0f, rho.x = 0.0f;
         if (bits >> s1 & 1) av.y = 0.0f, fv.y = 1.0f, rho.y = 0.0f;
@@ -527,43 +588,33 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
     wsum[par][warp][lane] = make_float4(P[0], P[VEC - 1], M[0], M[VEC - 1]);
     wfwd[par][warp][lane] = make_float2(Q[0], Q[VEC - 1]);
     __syncthreads();
-    float4 back = make_float4(1.0f, 1.0f, 0.0f, 0.0f), all = back;
-#pragma unroll
-    for (int w = kGatedWarps - 1; w >= 0; --w) {
-      if (w == warp) back = all;
-      const float4 m = wsum[par][w][lane];
-      all.z = through<START>(m.x, all.z, m.z);
-      all.w = through<START>(m.y, all.w, m.w);
-      all.x = times<START>(all.x, m.x);
-      all.y = times<START>(all.y, m.y);
+    // the steps behind this warp's; the first warp's, with its own, is the tile's
+    float4 back = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+    for (int w = kGatedWarps - 1; w > warp; --w) gated_compose<VEC, START>(back, wsum[par][w][lane]);
+    if (warp == 0) {
+      float4 all = back;
+      gated_compose<VEC, START>(all, make_float4(P[0], P[VEC - 1], M[0], M[VEC - 1]));
+      if (C > 1)
+        for (int w = 0; w < C; ++w) st_peer(&csum[par][rank][lane], w, all);
+      else
+        csum[par][0][lane] = all;
     }
-#pragma unroll
-    for (int w = 0; w < kGatedWarps - 1; ++w)
-      if (w < warp) {
-        const float4 m = wsum[par][w][lane];
-        const float2 x = wfwd[par][w][lane];
-        hs[0] = through<START>(m.x, hs[0], x.x);
-        if constexpr (VEC == 2) hs[1] = through<START>(m.y, hs[1], x.y);
-      }
+    for (int w = 0; w < warp; ++w) {
+      const float4 m = wsum[par][w][lane];
+      const float2 x = wfwd[par][w][lane];
+      hs[0] = through<START>(m.x, hs[0], x.x);
+      if constexpr (VEC == 2) hs[1] = through<START>(m.y, hs[1], x.y);
+    }
+    gated_exchange(C, warp == 0);
     float mb[VEC];  // adjoint behind the warp's steps
-    if (C > 1) {
-      if (warp < C) st_peer(&csum[par][rank][lane], warp, all);
-      cluster_arrive();
-      cluster_wait();
-      for (int w = 0; w < C; ++w) {
-        if (w == rank) {
+    for (int w = 0; w < C; ++w) {
+      if (w == rank) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) mb[e] = mu[e];
-        }
-        const float4 m = csum[par][w][lane];
-        mu[0] = through<START>(m.x, mu[0], m.z);
-        if constexpr (VEC == 2) mu[1] = through<START>(m.y, mu[1], m.w);
+        for (int e = 0; e < VEC; ++e) mb[e] = mu[e];
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) mb[e] = mu[e];
-      mu[0] = through<START>(all.x, mu[0], all.z);
-      if constexpr (VEC == 2) mu[1] = through<START>(all.y, mu[1], all.w);
+      const float4 m = csum[par][w][lane];
+      mu[0] = through<START>(m.x, mu[0], m.z);
+      if constexpr (VEC == 2) mu[1] = through<START>(m.y, mu[1], m.w);
     }
     mb[0] = through<START>(back.x, mb[0], back.z);
     if constexpr (VEC == 2) mb[1] = through<START>(back.y, mb[1], back.w);
@@ -686,9 +737,8 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const GatedParams p, fl
     const float r = sigmoid_f32(ga[e] + (p.ba ? ld_param(p.ba, c + e, p.d) : 0.0f));
     const float g = sigmoid_f32(gx[e] + (p.bx ? ld_param(p.bx, c + e, p.d) : 0.0f));
     float2 a, w;
-    decay2(f2(ld_param(p.A, c + e, p.d) * kLog2e * r), a, w);
-    const float wm = max_nan(w.x, kGatedMinW);
-    h[e] = fmaf(a.x, h[e], wm * rsqrt_approx(wm) * (g * u[e]));
+    decay2(f2(min_nan(ld_param(p.A, c + e, p.d) * kLog2e, 126.0f) * r), a, w);
+    h[e] = fmaf(a.x, h[e], w.x * rsqrt_approx(w.x) * (g * u[e]));
     y[e] = h[e];
     if constexpr (GATE) y[e] *= silu_f32(z[e]);
   }
