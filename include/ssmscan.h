@@ -511,18 +511,18 @@ ssm_status ss2d_cross_merge(const void *ys, void *y, int64_t b, int64_t H,
  *     a = exp(A[d] * r)
  *     h = a * h + sqrt(1 - a^2) * g * u[i,t,d]      (h = g * u where a sequence starts)
  *     y[i,t,d] = z ? h * silu(z[i,t,d]) : h
- * and h_last[i,d] = h after the last step.  A holds log decays: values <= 0
- * (above 0 the decay exceeds 1 and the input factor is 0).
+ * and h_last[i,d] = h after the last step.  A holds log decays, values <= 0
+ * (above 0 the root has no value: NaN).
  *
  *   u, gate_a, gate_x, z, y   device rows (b L, d_in), dtype; z nullable
  *   A                         device fp32 (d_in)
  *   bias_a, bias_x            device fp32 (d_in), nullable (0)
  *   h0, h_last                device fp32 (b, d_in), nullable; h_last may equal h0
  *   chunk_states              device fp32, nullable: the state in front of every
- *                             64th step, (b, ceil(L / 64), d_in), for
+ *                             32nd step, (b, ceil(L / 32), d_in), for
  *                             ssm_gated_scan_bwd; chunk_states_bytes >=
  *                             ssm_gated_scan_states_bytes(b, L, d_in)
- * Arithmetic and state are fp32; y is rounded once.
+ * Arithmetic and state are fp32; y is rounded once.  L <= 2^30.
  */
 ssm_status ssm_gated_scan_fwd(const void *u, int64_t u_ld, const void *gate_a, int64_t gate_a_ld,
                               const void *gate_x, int64_t gate_x_ld, const float *A,
@@ -532,7 +532,7 @@ ssm_status ssm_gated_scan_fwd(const void *u, int64_t u_ld, const void *gate_a, i
                               size_t chunk_states_bytes, int64_t b, int64_t L, int64_t d_in,
                               ssm_dtype dtype, ssm_stream_t stream);
 
-/* Bytes of chunk_states: b * ceil(L / 64) * d_in * 4; (size_t)-1 for invalid sizes. */
+/* Bytes of chunk_states: b * ceil(L / 32) * d_in * 4; (size_t)-1 for invalid sizes. */
 size_t ssm_gated_scan_states_bytes(int64_t b, int64_t L, int64_t d_in);
 
 /*

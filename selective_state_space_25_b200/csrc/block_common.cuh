@@ -7,7 +7,7 @@
 namespace ssm {
 
 // Steps between the states ssm_gated_scan_fwd keeps for its backward.
-constexpr int kGatedChunk = 64;
+constexpr int kGatedChunk = 32;
 
 // Largest convolution width.
 constexpr int kMaxConv = 8;
@@ -42,12 +42,14 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 
 __device__ __forceinline__ float2 f2(float v) { return make_float2(v, v); }
 
-// Decays of two elements from x = A r log2(e), at most 126: a = 2^x and w = 1 -
-// a^2 (or kDecayMinW where that is larger), both with the accuracy the recurrence
-// needs.  x = j + s with j = rint(x), S = 2^j: a = S + S p, a - 1 = S p + (S - 1)
-// with p = 2^s - 1 the polynomial; for j = 0 that is p itself, below it S - 1 is
-// exact and no smaller than 1/2.  w = -(a - 1)(a + 1).
-constexpr float kDecayMinW = 1e-36f;  // its root stands under 1 / f
+// Decays of two elements from x = A r log2(e) <= 0: a = 2^x and w = 1 - a^2 +
+// kDecayMinW, both with the accuracy the recurrence needs.  x = j + s with j =
+// rint(x), S = 2^j: a = S + S p, a - 1 = S p + (S - 1) with p = 2^s - 1 the
+// polynomial; for j = 0 that is p itself, below it S - 1 is exact and no smaller
+// than 1/2.  w = -(a - 1)(a + 1); the 1e-36 keeps its inverse root finite where a
+// is 1.  x > 0 (A > 0, outside the operator's domain) makes w negative and what
+// its root enters NaN.
+constexpr float kDecayMinW = 1e-36f;
 __device__ __forceinline__ void decay2(float2 x, float2 &a, float2 &w) {
   x.x = max_nan(x.x, -126.0f);
   x.y = max_nan(x.y, -126.0f);
@@ -64,9 +66,7 @@ __device__ __forceinline__ void decay2(float2 x, float2 &a, float2 &w) {
                                __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000));
   a = __ffma2_rn(S, p, S);
   const float2 m = __ffma2_rn(S, p, __fadd2_rn(S, f2(-1.0f)));
-  w = __fmul2_rn(m, __ffma2_rn(m, f2(-1.0f), f2(-2.0f)));
-  w.x = max_nan(w.x, kDecayMinW);
-  w.y = max_nan(w.y, kDecayMinW);
+  w = __ffma2_rn(m, __ffma2_rn(m, f2(-1.0f), f2(-2.0f)), f2(kDecayMinW));
 }
 
 // ------------------------------------------------------- element access

@@ -169,26 +169,35 @@ bool vec_rows(int64_t vec, size_t es, int64_t d, std::initializer_list<std::pair
 // --------------------------------------------------------- gated recurrence
 int64_t gated_chunks(int64_t L) { return (L + ssm::kGatedChunk - 1) / ssm::kGatedChunk; }
 
-// CTAs of a cluster, each a tile of 64 steps at a time.  An SM's time goes as the
-// CTAs it gets times the rounds of tiles each takes; the smallest cluster within
-// a tenth of the least (each doubling costs a wider exchange).
+// Parts of a warp (S) and CTAs of a cluster (C).  A CTA's round is 64 S steps of
+// 1 / S of the channels, the same work whatever S; an SM's time goes as the rounds
+// of a CTA times the CTAs it holds, or times two where it holds fewer (a round's
+// own latency), a quarter more with clusters, whose CTAs wait for each other in
+// every round.  Of equal ones the one with the widest rows.  Measured (B200, bf16, b
+// = 8, L = 2048, d = 1536, forward, us): see gated_scan.cuh.
 struct GatedPlan {
-  int ctiles, csize;
+  int parts, ctiles, csize;
 };
 GatedPlan gated_plan(int64_t b, int64_t L, int64_t d, int channels) {
-  const int64_t tiles = gated_chunks(L), sms = device_sms();
-  GatedPlan g;
-  g.ctiles = (int)((d + channels - 1) / channels);
-  int64_t cost[4], least = -1;
-  for (int k = 0; k < 4; ++k) {
-    const int64_t c = 1 << k;
-    cost[k] = ((b * g.ctiles * c + sms - 1) / sms) * ((tiles + c - 1) / c);
-    if (least < 0 || cost[k] < least) least = cost[k];
-  }
-  int k = 0;
-  while (10 * cost[k] > 11 * least) ++k;
-  g.csize = 1 << k;
-  return g;
+  const int64_t sms = device_sms();
+  GatedPlan best{1, 1, 1};
+  int64_t least = -1;
+  for (int s = 1; s <= 4; s *= 2)
+    for (int c = 1; c <= ssm::kGatedMaxCluster; c *= 2) {
+      const int64_t tiles = (d + channels / s - 1) / (channels / s);
+      const int64_t rounds = (L + 64 * s * c - 1) / (64 * s * c);
+      const int64_t held = (b * tiles * c + sms - 1) / sms;
+      const int64_t cost = rounds * (held > 2 ? held : 2) * (c > 1 ? 5 : 4);
+      if (least < 0 || cost < least) {
+        least = cost;
+        best = GatedPlan{s, (int)tiles, c};
+      }
+    }
+#ifdef SSM_GS
+  best.parts = SSM_GS, best.csize = SSM_GC;
+  best.ctiles = (int)((d + channels / SSM_GS - 1) / (channels / SSM_GS));
+#endif
+  return best;
 }
 int64_t gated_bwd_parts(int64_t b, int64_t L, int64_t d) {  // of whichever type
   const int f = gated_plan(b, L, d, 32).csize, h = gated_plan(b, L, d, 64).csize;
@@ -196,9 +205,10 @@ int64_t gated_bwd_parts(int64_t b, int64_t L, int64_t d) {  // of whichever type
 }
 
 template <auto Kernel, typename P>
-ssm_status launch_gated(const P &p, int64_t b, const GatedPlan &g, int smem, cudaStream_t st,
+ssm_status launch_gated(const P &p, int64_t b, const GatedPlan &g, int smem, int most, cudaStream_t st,
                         const char *what) {
-  if (ssm_status s = ensure_smem<Kernel>(smem, what)) return s;
+  // the most any call of this kernel takes, set once
+  if (ssm_status s = ensure_smem<Kernel>(most, what)) return s;
   if (b > kMaxGrid / ((int64_t)g.ctiles * g.csize))
     return fail(SSM_ERR_UNSUPPORTED, "%s: b * d_in too large for one grid", what);
   cudaLaunchConfig_t cfg = {};
@@ -223,21 +233,23 @@ ssm_status launch_gated(const P &p, int64_t b, const GatedPlan &g, int smem, cud
 template <typename T, bool ASYNC, bool GATE>
 ssm_status gated_fwd_t(ssm::GatedParams p, cudaStream_t st) {
   const GatedPlan g = gated_plan(p.b, p.L, p.d, 32 * ssm::gated_vec<T>());
-  p.ctiles = g.ctiles, p.csize = g.csize;
-  constexpr int smem = ssm::gated_smem(GATE ? 4 : 3);
+  p.parts = g.parts, p.ctiles = g.ctiles, p.csize = g.csize;
+  const int smem = ssm::gated_smem(GATE ? 4 : 3, ssm::kGatedFwdSteps, g.csize);
+  constexpr int most = ssm::gated_smem(GATE ? 4 : 3, ssm::kGatedFwdSteps, ssm::kGatedMaxCluster);
   if (p.start)
-    return launch_gated<ssm::gated_fwd_kernel<T, ASYNC, GATE, true>>(p, p.b, g, smem, st, "ssm_gated_scan_fwd");
-  return launch_gated<ssm::gated_fwd_kernel<T, ASYNC, GATE, false>>(p, p.b, g, smem, st, "ssm_gated_scan_fwd");
+    return launch_gated<ssm::gated_fwd_kernel<T, ASYNC, GATE, true>>(p, p.b, g, smem, most, st, "ssm_gated_scan_fwd");
+  return launch_gated<ssm::gated_fwd_kernel<T, ASYNC, GATE, false>>(p, p.b, g, smem, most, st, "ssm_gated_scan_fwd");
 }
 template <typename T, bool ASYNC, bool GATE>
 ssm_status gated_bwd_t(ssm::GatedBwdParams q, int64_t *parts, cudaStream_t st) {
   const GatedPlan g = gated_plan(q.f.b, q.f.L, q.f.d, 32 * ssm::gated_vec<T>());
-  q.f.ctiles = g.ctiles, q.f.csize = g.csize;
+  q.f.parts = g.parts, q.f.ctiles = g.ctiles, q.f.csize = g.csize;
   *parts = q.f.b * g.csize;
-  constexpr int smem = ssm::gated_smem(GATE ? 5 : 4);
+  const int smem = ssm::gated_smem(GATE ? 5 : 4, ssm::kGatedBwdSteps, g.csize);
+  constexpr int most = ssm::gated_smem(GATE ? 5 : 4, ssm::kGatedBwdSteps, ssm::kGatedMaxCluster);
   if (q.f.start)
-    return launch_gated<ssm::gated_bwd_kernel<T, ASYNC, GATE, true>>(q, q.f.b, g, smem, st, "ssm_gated_scan_bwd");
-  return launch_gated<ssm::gated_bwd_kernel<T, ASYNC, GATE, false>>(q, q.f.b, g, smem, st, "ssm_gated_scan_bwd");
+    return launch_gated<ssm::gated_bwd_kernel<T, ASYNC, GATE, true>>(q, q.f.b, g, smem, most, st, "ssm_gated_scan_bwd");
+  return launch_gated<ssm::gated_bwd_kernel<T, ASYNC, GATE, false>>(q, q.f.b, g, smem, most, st, "ssm_gated_scan_bwd");
 }
 // Rows in 16-byte pieces (inputs) and VEC elements (outputs) where all allow it.
 template <typename T> ssm_status gated_fwd_any(const ssm::GatedParams &p, cudaStream_t st) {
@@ -281,6 +293,7 @@ ssm_status check_gated(const char *what, Args &a, const ssm::GatedParams &p, ssm
   if (ssm_status s = bad_dtype(what, dtype)) return s;
   if (!sizes_ok({p.b, p.L, p.d}))
     return fail(SSM_ERR_INVALID_ARG, "%s: negative size or sizes that overflow int64", what);
+  if (p.L > (1 << 30)) return fail(SSM_ERR_UNSUPPORTED, "%s: L above 2^30", what);
   const int64_t R = p.b * p.L;
   if (R > 0 && p.d > 0 && (!p.u || !p.ga || !p.gx || !p.A))
     return fail(SSM_ERR_INVALID_ARG, "%s: u, gate_a, gate_x and A are required", what);

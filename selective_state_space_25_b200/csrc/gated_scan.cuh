@@ -5,16 +5,18 @@
 //   h_t = a h_{t-1} + f g u          (h_t = g u where a sequence starts)
 //
 // Split over time.  A step is the map h -> a h + x, and maps compose: steps
-// taken together are h -> P h + Q with P the product of their decays.  A CTA
-// takes 32 VEC channels (128 bytes of a row) and walks tiles of kGatedChunk = 64
-// steps; in a tile each of its 8 warps takes 8 steps, a lane VEC channels of
-// them, and forms its decays and drives and (P, Q) in registers.  The warps'
-// (P, Q) go through shared memory; each warp composes those in front of it onto
-// the tile's start state and then replays its 8 steps from registers.  So every
-// input is read once and nothing waits on more than 8 sequential steps, where a
-// thread per channel waits on L.  Where b * d alone gives too few CTAs, up to 8
-// CTAs of a cluster take consecutive tiles at once and exchange their tiles'
-// (P, Q) through each other's shared memory.
+// taken together are h -> P h + Q with P the product of their decays.  A CTA's 8
+// warps walk tiles of 64 S steps: a lane takes VEC channels and 8 steps, 32 / S
+// lanes side by side the CTA's channels, the S parts of a warp and the warps
+// consecutive steps.  A lane forms its decays and drives and their (P, Q) in
+// registers; the parts of a warp combine by shuffles and the warps through shared
+// memory; each composes what lies in front of it onto the tile's start state and
+// then replays its 8 steps from registers.  So every input is read once and
+// nothing waits on more than 8 sequential steps, where a thread per channel waits
+// on L.  S (1, 2, 4: 128, 64, 32 bytes of a row for a CTA) trades channels for
+// steps until there are CTAs enough; where that is not enough, up to 8 CTAs of a
+// cluster take consecutive tiles at once and exchange the tiles' (P, Q) through
+// each other's shared memory (gated_plan).
 //
 // The adjoint is the same recurrence backwards: mu_t = a_t (dout_t + mu_{t+1}) is
 // what step t hands to step t - 1, so the backward composes (P, mu) of tiles from
@@ -37,6 +39,7 @@ struct GatedParams {
   int64_t y_ld;
   float *chunk_h;
   int64_t b, L, d;
+  int parts;    // S: parts of a warp
   int ctiles;   // CTAs across the channels
   int csize;    // CTAs of a cluster: tiles taken at once
 };
@@ -52,19 +55,34 @@ struct GatedBwdParams {
   float *part;  // (b * csize, 3, d): sums of dA, dbias_a, dbias_x
 };
 
-constexpr int kGatedWarps = 8, kGatedSteps = 8;  // warps of a CTA, steps of a warp
+constexpr int kGatedWarps = 8;  // of a CTA
 constexpr int kGatedThreads = 32 * kGatedWarps;
-static_assert(kGatedWarps * kGatedSteps == kGatedChunk, "a tile is a chunk");
+// Steps of a lane in a tile, and CTAs an SM holds.
+#ifndef SSM_GF
+#define SSM_GF 2
+#endif
+#ifndef SSM_GB
+#define SSM_GB 2
+#endif
+#ifndef SSM_GFS
+#define SSM_GFS 8
+#endif
+constexpr int kGatedFwdSteps = SSM_GFS, kGatedBwdSteps = 4;
+static_assert(kGatedWarps * kGatedBwdSteps == kGatedChunk && 2 * kGatedFwdSteps <= kGatedChunk,
+              "a backward tile is S chunks, a forward warp starts at most one");
 constexpr int kGatedMaxCluster = 8;
 constexpr int kGatedRowBytes = 128;
-// Staged bytes of a tensor's 8 rows for one warp.
-constexpr int kGatedStage = kGatedSteps * kGatedRowBytes;
 
 // Channels a lane takes: 32 VEC channels are 128 bytes.
 template <typename T> constexpr int gated_vec() { return 4 / (int)sizeof(T); }
 
-// Shared memory of a CTA that stages NT tensors two tiles deep.
-constexpr int gated_smem(int nt) { return 2 * nt * kGatedWarps * kGatedStage; }
+// Dynamic shared memory of a CTA: NT tensors' rows of two tiles, then the
+// compositions of the cluster's tiles, for two rounds.
+constexpr int gated_stage(int nt, int steps) { return nt * kGatedWarps * steps * kGatedRowBytes; }
+constexpr int kGatedStages = 2;
+constexpr int gated_smem(int nt, int steps, int csize) {
+  return kGatedStages * gated_stage(nt, steps) + 2 * csize * 32 * 16;
+}
 
 // ------------------------------------------------------------- clusters
 __device__ __forceinline__ void cluster_arrive() {
@@ -110,6 +128,37 @@ template <bool START> __device__ __forceinline__ float times(float P, float a) {
   return START && (P == 0.0f || a == 0.0f) ? 0.0f : r;
 }
 
+// States of VEC channels after the map m, (P, P, Q, Q).
+template <int VEC, bool START> __device__ __forceinline__ void gated_apply(float (&h)[VEC], float4 m) {
+  if constexpr (VEC == 2 && !START) {
+    const float2 r = __ffma2_rn(make_float2(m.x, m.y), make_float2(h[0], h[1]), make_float2(m.z, m.w));
+    h[0] = r.x, h[1] = r.y;
+  } else {
+    h[0] = through<START>(m.x, h[0], m.z);
+    if constexpr (VEC == 2) h[1] = through<START>(m.y, h[1], m.w);
+  }
+}
+// Flat elements 2 q and 2 q + 1 of a lane (one step of two channels, or two steps
+// of one) taken into the state h and the product P of the decays.
+template <int VEC, bool START>
+__device__ __forceinline__ void gated_step2(float (&h)[VEC], const float *a, const float *x) {
+  if constexpr (VEC == 2) {
+    gated_apply<2, START>(h, make_float4(a[0], a[1], x[0], x[1]));
+  } else {
+    h[0] = through<START>(a[0], h[0], x[0]);
+    h[0] = through<START>(a[1], h[0], x[1]);
+  }
+}
+template <int VEC, bool START> __device__ __forceinline__ void gated_prod2(float (&P)[VEC], const float *a) {
+  if constexpr (VEC == 2 && !START) {
+    const float2 r = __fmul2_rn(make_float2(P[0], P[1]), make_float2(a[0], a[1]));
+    P[0] = r.x, P[1] = r.y;
+  } else {
+    P[0] = times<START>(P[0], a[0]);
+    P[VEC - 1] = times<START>(P[VEC - 1], a[1]);
+  }
+}
+
 // m after `front`, both (P, P, Q, Q) of a lane's channels.
 template <int VEC, bool START> __device__ __forceinline__ void gated_compose(float4 &front, float4 m) {
   front.z = through<START>(m.x, front.z, m.z);
@@ -120,22 +169,43 @@ template <int VEC, bool START> __device__ __forceinline__ void gated_compose(flo
   }
 }
 
+// (P, P, Q, Q) of another lane.
+__device__ __forceinline__ float4 shfl4(float4 v, int lane) {
+  return make_float4(__shfl_sync(~0u, v.x, lane), __shfl_sync(~0u, v.y, lane),
+                     __shfl_sync(~0u, v.z, lane), __shfl_sync(~0u, v.w, lane));
+}
+
+// The parts of a warp in the order they are taken (FIRST: part 0 first, else the
+// last part first): own becomes the composition of the parts in front of this
+// lane's, all that of the warp's.
+template <int VEC, bool START, bool FIRST>
+__device__ __forceinline__ void gated_parts(int S, int lane, float4 &own, float4 &all) {
+  const int lc = 32 / S, part = lane / lc, l = lane % lc;
+  const float4 mine = own;
+  own = all = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+  if (S == 1) {
+    all = mine;
+    return;
+  }
+  for (int k = 0; k < S; ++k) {
+    const int s = FIRST ? k : S - 1 - k;
+    const float4 m = shfl4(mine, s * lc + l);
+    if (s == part) own = all;
+    gated_compose<VEC, START>(all, m);
+  }
+}
+
 // Makes the tiles' compositions, which one warp of each CTA wrote, known to all
 // of the cluster.  Only that warp releases at cluster scope (a release waits for
 // a warp's global stores too): its release covers what the CTA's other warps
 // read of the buffer two rounds ago, which the round's __syncthreads ordered
 // before it.
-__device__ __forceinline__ void gated_exchange(int C, bool writer) {
-  if (C == 1) {
-    __syncthreads();
-    return;
-  }
+__device__ __forceinline__ void gated_arrive(bool writer) {
   __syncwarp();
   if (writer)
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   else
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  cluster_wait();
 }
 
 // Per-lane constants: VEC channels from c0 (the pair's two for VEC = 2, one
@@ -158,50 +228,51 @@ template <int VEC>
 __device__ __forceinline__ GatedLane gated_lane(const GatedParams &p, int64_t c) {
   GatedLane l;
   l.A2 = mul2(lane_pair<VEC>(p.A, c, p.d), f2(kLog2e));
-  l.A2 = make_float2(min_nan(l.A2.x, 126.0f), min_nan(l.A2.y, 126.0f));
   l.na = mul2(lane_pair<VEC>(p.ba, c, p.d), f2(-kLog2e));
   l.nx = mul2(lane_pair<VEC>(p.bx, c, p.d), f2(-kLog2e));
   return l;
 }
 
 // ----------------------------------------------------------------- staging
-// One tensor's rows for a warp: 8 rows of 128 bytes a tile, `step` bytes to the
-// next tile's.  ASYNC: 16-byte cp.async (rows 16-byte aligned, d a multiple of 16
-// bytes), lane l the piece l % 8 of rows l / 8 and l / 8 + 4; else element loads.
-// Rows past the end and channels past d become zeros.
-template <typename T, bool ASYNC> struct GatedSrc {
+// One tensor's rows for a warp, `step` bytes to the next tile's.  In shared memory
+// step k of all parts lies side by side, 128 bytes, lane l's channels at 4 l (so
+// that a warp reads each bank once).  ASYNC: 16-byte cp.async (rows 16-byte
+// aligned, d a multiple of 16 bytes), lane l the 16 bytes l % 8 of steps l / 8 (and
+// l / 8 + 4); else element loads.  Rows past the end and channels past d become zeros.
+template <typename T, bool ASYNC, int STEPS> struct GatedSrc {
   const char *p;      // the lane's first element of the next tile
   int64_t ld, step;   // bytes
   const char *lo, *hi;  // the buffer (debug-bounds build)
+  // row: the warp's first
   __device__ __forceinline__ void init(const void *src, int64_t ld_, int64_t row, int64_t tile_rows,
-                                       int64_t c0, int lane, int64_t rows, int64_t d) {
-    constexpr int E = 16 / (int)sizeof(T);
+                                       int64_t c0, int lane, int64_t rows, int64_t d, int S) {
     ld = ld_ * (int64_t)sizeof(T);
     step = tile_rows * ld;
     lo = static_cast<const char *>(src);
     hi = lo + extent(rows, d, ld_) * (int64_t)sizeof(T);
+    const int lc = 32 / S, pc = 8 / S;  // lanes, 16-byte pieces of a part
     p = lo + row * ld + c0 * (int64_t)sizeof(T) +
-        (ASYNC ? lane / 8 * ld + lane % 8 * 16 : lane * gated_vec<T>() * (int64_t)sizeof(T));
-    (void)E;
+        (ASYNC ? (lane % 8 / pc * STEPS + lane / 8) * ld + lane % 8 % pc * 16
+               : lane / lc * STEPS * ld + lane % lc * gated_vec<T>() * (int64_t)sizeof(T));
   }
-  // n rows of this tile; bytes: 16 where the lane's piece lies in front of d, else
-  // 0 (elements: how many of the lane's do)
+  // n rows of this tile for the part whose bytes the lane copies; bytes: 16 where
+  // its piece lies in front of d, else 0 (elements: how many of the lane's do)
   __device__ __forceinline__ void fetch(char *s, int n, int bytes, int lane) {
     if constexpr (ASYNC) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < STEPS / 4; ++j) {
         const char *q = p + 4 * j * ld;
         int b = bytes;
-        if (n < kGatedSteps && lane / 8 + 4 * j >= n) b = 0;
+        if (n < STEPS && lane / 8 + 4 * j >= n) b = 0;
         if (b && !in_bounds(q - lo, hi - lo - 15, kBndAct)) b = 0;
-        if (n < kGatedSteps && !b) q = lo;
+        if (n < STEPS && !b) q = lo;
         cp_async16(s + j * 512 + lane * 16, q, b);
       }
     } else {
       constexpr int VEC = gated_vec<T>();
-      T v[kGatedSteps][VEC];
+      T v[STEPS][VEC];
 #pragma unroll
-      for (int r = 0; r < kGatedSteps; ++r)
+      for (int r = 0; r < STEPS; ++r)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const char *q = p + r * ld + e * (int)sizeof(T);
@@ -209,7 +280,7 @@ template <typename T, bool ASYNC> struct GatedSrc {
                         ? *reinterpret_cast<const T *>(q) : T(0.0f);
         }
 #pragma unroll
-      for (int r = 0; r < kGatedSteps; ++r)
+      for (int r = 0; r < STEPS; ++r)
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
           reinterpret_cast<T *>(s + r * kGatedRowBytes)[lane * VEC + e] = v[r][e];
@@ -219,9 +290,9 @@ template <typename T, bool ASYNC> struct GatedSrc {
 };
 // The `bytes` of fetch for a lane.
 template <typename T, bool ASYNC>
-__device__ __forceinline__ int gated_piece(int64_t c0, int lane, int64_t d) {
-  if constexpr (ASYNC) return c0 + lane % 8 * (16 / (int)sizeof(T)) < d ? 16 : 0;
-  const int64_t left = d - c0 - lane * gated_vec<T>();
+__device__ __forceinline__ int gated_piece(int64_t c0, int lane, int64_t d, int S) {
+  if constexpr (ASYNC) return c0 + lane % 8 % (8 / S) * (16 / (int)sizeof(T)) < d ? 16 : 0;
+  const int64_t left = d - c0 - lane % (32 / S) * gated_vec<T>();
   return left < 0 ? 0 : left < gated_vec<T>() ? (int)left : gated_vec<T>();
 }
 
@@ -238,19 +309,34 @@ __device__ __forceinline__ float2 staged_pair(const char *s, int k, int lane) {
   }
 }
 
-// Stores flat elements of step s: VEC channels from c.
-template <typename T, bool ASYNC>
-__device__ __forceinline__ void store_step(void *p, int64_t ld, int64_t row, int64_t c, int64_t d,
-                                           int64_t ext, const float *v) {
-  constexpr int VEC = gated_vec<T>();
-  if constexpr (ASYNC) {
-    if (c < d) st_vec<T, VEC>(p, row * ld + c, ext, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      if (c + e < d) st_vec<T, 1>(p, row * ld + c + e, ext, v + e);
+// An output's place: the lane's channels in the first of its steps of a tile,
+// `step` elements to the next tile's.
+template <typename T, bool ASYNC> struct GatedDst {
+  T *p;
+  int64_t ld, step;
+  T *lo;
+  int64_t n;  // elements of the buffer (debug-bounds build)
+  __device__ __forceinline__ void init(void *dst, int64_t ld_, int64_t row, int64_t tile_rows, int64_t c,
+                                       int64_t rows, int64_t d) {
+    lo = static_cast<T *>(dst);
+    n = extent(rows, d, ld_);
+    ld = ld_;
+    step = tile_rows * ld_;
+    p = lo + (row * ld_ + c);
   }
-}
+  // VEC channels of step t of the tile, `left` of them in front of d
+  __device__ __forceinline__ void store(int t, int left, const float *v) const {
+    constexpr int VEC = gated_vec<T>();
+    T *q = p + t * ld;
+    if constexpr (ASYNC) {
+      if (left > 0 && in_bounds(q - lo, n - (VEC - 1), kBndAct)) st_vec<T, VEC>(q, 0, VEC, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e < left && in_bounds(q + e - lo, n, kBndAct)) st_vec<T, 1>(q, e, VEC, v + e);
+    }
+  }
+};
 
 // ----------------------------------------------------------------- forward
 // Grid: csize * ctiles * b CTAs in clusters of csize.  SFU operations an element:
@@ -258,31 +344,38 @@ __device__ __forceinline__ void store_step(void *p, int64_t ld, int64_t row, int
 // w = 1 - a^2), two more with z; the decay's exponential is a polynomial
 // (decay2), which also gives 1 - a without cancellation.
 template <typename T, bool ASYNC, bool GATE, bool START>
-__global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const GatedParams p) {
-  constexpr int VEC = gated_vec<T>(), E = kGatedSteps * VEC, NT = GATE ? 4 : 3;
+__global__ void __launch_bounds__(kGatedThreads, SSM_GF) gated_fwd_kernel(const GatedParams p) {
+  constexpr int STEPS = kGatedFwdSteps, VEC = gated_vec<T>(), E = STEPS * VEC, NT = GATE ? 4 : 3;
+  constexpr int kRows = STEPS * kGatedRowBytes;  // bytes of a tensor's rows for a warp
   extern __shared__ __align__(16) char stage[];
   __shared__ float4 wsum[2][kGatedWarps][32];       // (P, Q) of the warps' steps
-  __shared__ float4 csum[2][kGatedMaxCluster][32];  // (P, Q) of the cluster's tiles
+  float4 *const csum =
+      reinterpret_cast<float4 *>(stage + kGatedStages * gated_stage(NT, STEPS));  // [2][C][32]
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int C = p.csize, rank = (int)(blockIdx.x % (unsigned)C);
   const unsigned grp = blockIdx.x / (unsigned)C;
-  const int64_t c0 = (grp % (unsigned)p.ctiles) * (int64_t)(32 * VEC), i = grp / (unsigned)p.ctiles;
-  const int64_t c = c0 + lane * VEC;
-  const int64_t R = p.b * p.L, nT = (p.L + kGatedChunk - 1) / kGatedChunk;
-  const int iters = (int)((nT + C - 1) / C);
-  char *mine = stage + warp * NT * kGatedStage;
-  constexpr int kHalf = NT * kGatedWarps * kGatedStage;
+  const int S = p.parts, lc = 32 / S, part = lane / lc;
+  const int64_t c0 = (grp % (unsigned)p.ctiles) * (int64_t)(lc * VEC), i = grp / (unsigned)p.ctiles;
+  const int64_t c = c0 + lane % lc * VEC;
+  const int64_t R = p.b * p.L;
+  const int L = (int)p.L, tile_rows = C * S * kGatedWarps * STEPS;  // of the cluster
+  const int iters = (L + tile_rows - 1) / tile_rows;
+  char *mine = stage + warp * NT * kRows;
+  constexpr int kHalf = gated_stage(NT, STEPS);
   const GatedLane k = gated_lane<VEC>(p, c);
-  const int64_t t_first = rank * kGatedChunk + warp * kGatedSteps;  // the warp's first step
-  const int64_t row0 = i * p.L + t_first;
-  const int64_t tile_rows = (int64_t)C * kGatedChunk;
-  GatedSrc<T, ASYNC> su, sa, sg, sz;
-  su.init(p.u, p.u_ld, row0, tile_rows, c0, lane, R, p.d);
-  sa.init(p.ga, p.ga_ld, row0, tile_rows, c0, lane, R, p.d);
-  sg.init(p.gx, p.gx_ld, row0, tile_rows, c0, lane, R, p.d);
-  if constexpr (GATE) sz.init(p.z, p.z_ld, row0, tile_rows, c0, lane, R, p.d);
-  const int piece = gated_piece<T, ASYNC>(c0, lane, p.d);
-  const int64_t xy = extent(R, p.d, p.y_ld);
+  // the warp's first step, the lane's, and that of the part it copies for
+  const int t_warp = (rank * kGatedWarps + warp) * (S * STEPS);
+  const int t_lane = t_warp + part * STEPS;
+  const int t_copy = ASYNC ? t_warp + lane % 8 / (8 / S) * STEPS : t_lane;
+  GatedSrc<T, ASYNC, STEPS> su, sa, sg, sz;
+  su.init(p.u, p.u_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
+  sa.init(p.ga, p.ga_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
+  sg.init(p.gx, p.gx_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
+  if constexpr (GATE) sz.init(p.z, p.z_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
+  const int piece = gated_piece<T, ASYNC>(c0, lane, p.d, S);
+  GatedDst<T, ASYNC> dy;
+  dy.init(p.y, p.y_ld, i * p.L + t_lane, tile_rows, c, R, p.d);
+  const int left = (int)(p.d - c < VEC ? p.d - c : VEC);  // channels in front of d
   float h[VEC];  // state in front of the cluster's next tiles
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
@@ -290,23 +383,24 @@ __global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const Gated
     if (p.h0 && c + e < p.d && in_bounds(i * p.d + c + e, p.b * p.d, kBndState))
       h[e] = p.h0[i * p.d + c + e];
   }
-  unsigned flag = 0;  // lane r: whether a sequence starts at the next tile's row r
-  // the warp's rows of its CTA's tile of round `it`
-  const auto rows_of = [&](int it) {
-    const int64_t left = p.L - t_first - it * tile_rows;
-    return left >= kGatedSteps ? kGatedSteps : left > 0 ? (int)left : 0;
+  unsigned flag = 0;  // lane r: whether a sequence starts at the warp's next row r
+  // rows from step t on of round `it`
+  const auto rows_of = [&](int t, int it) {
+    const int left = L - t - it * tile_rows;
+    return left >= STEPS ? STEPS : left > 0 ? left : 0;
   };
   const auto fetch = [&](int it) {
     if (it < iters) {
-      const int n = rows_of(it);
+      const int n = rows_of(t_copy, it);
       char *s = mine + (it & 1) * kHalf;
       su.fetch(s, n, piece, lane);
-      sa.fetch(s + kGatedStage, n, piece, lane);
-      sg.fetch(s + 2 * kGatedStage, n, piece, lane);
-      if constexpr (GATE) sz.fetch(s + 3 * kGatedStage, n, piece, lane);
+      sa.fetch(s + kRows, n, piece, lane);
+      sg.fetch(s + 2 * kRows, n, piece, lane);
+      if constexpr (GATE) sz.fetch(s + 3 * kRows, n, piece, lane);
       if (START) {
-        const int64_t r = row0 + it * tile_rows + lane;
-        flag = lane < n && in_bounds(r, R, kBndAct) ? p.start[r] : 0;
+        const int t = t_warp + it * tile_rows + lane;
+        const int64_t r = i * p.L + t;
+        flag = lane < S * STEPS && t < L && in_bounds(r, R, kBndAct) ? p.start[r] : 0;
       }
     }
     cp_async_commit();
@@ -317,19 +411,20 @@ __global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const Gated
   }
   fetch(0);
   for (int it = 0; it < iters; ++it) {
-    const unsigned bits = START ? __ballot_sync(~0u, flag != 0) : 0;
+    const unsigned bits = START ? __ballot_sync(~0u, flag != 0) >> (part * STEPS) & ((1u << STEPS) - 1) : 0;
+    const bool any = START && __any_sync(~0u, bits != 0);
     __syncwarp();  // the other half's rows are no longer read
     fetch(it + 1);
     cp_async_wait<1>();
     __syncwarp();
-    const int n = rows_of(it);
+    const int n = rows_of(t_lane, it);
     const char *s = mine + (it & 1) * kHalf;
     // decays and drives of the warp's steps, and their composition
     float a[E], x[E];
 #pragma unroll
     for (int q = 0; q < E / 2; ++q) {
-      const float2 er = ex2_2(fma2(staged_pair<T>(s + kGatedStage, q, lane), f2(-kLog2e), k.na));
-      const float2 eg = ex2_2(fma2(staged_pair<T>(s + 2 * kGatedStage, q, lane), f2(-kLog2e), k.nx));
+      const float2 er = ex2_2(fma2(staged_pair<T>(s + kRows, q, lane), f2(-kLog2e), k.na));
+      const float2 eg = ex2_2(fma2(staged_pair<T>(s + 2 * kRows, q, lane), f2(-kLog2e), k.nx));
       const float2 r = rcp_2(__fadd2_rn(er, f2(1.0f)));
       const float2 q1 = __fadd2_rn(eg, f2(1.0f));
       float2 av, w;
@@ -338,7 +433,7 @@ __global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const Gated
       // f g = w / sqrt(w (1 + e^-x)^2)
       const float2 fg = mul2(w, rsqrt_2(mul2(mul2(w, q1), q1)));
       float2 xv = mul2(fg, u);
-      if (START && bits) {
+      if (START && any) {
         const int s0 = 2 * q / VEC, s1 = (2 * q + 1) / VEC;
         if (bits >> s0 & 1) av.x = 0.0f, xv.x = u.x * rcp_approx(q1.x);
         if (bits >> s1 & 1) av.y = 0.0f, xv.y = u.y * rcp_approx(q1.y);
@@ -346,80 +441,95 @@ __global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const Gated
       a[2 * q] = av.x, a[2 * q + 1] = av.y;
       x[2 * q] = xv.x, x[2 * q + 1] = xv.y;
     }
-    if (n < kGatedSteps) {  // steps past the end change nothing
+    if (n < STEPS) {  // steps past the end change nothing
 #pragma unroll
       for (int q = 0; q < E; ++q)
         if (q / VEC >= n) a[q] = 1.0f, x[q] = 0.0f;
     }
     float P[VEC], Q[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) P[e] = a[e], Q[e] = x[e];
+    for (int e = 0; e < VEC; ++e) P[e] = 1.0f, Q[e] = 0.0f;
 #pragma unroll
-    for (int q = VEC; q < E; ++q) {
-      Q[q % VEC] = through<START>(a[q], Q[q % VEC], x[q]);
-      P[q % VEC] = times<START>(P[q % VEC], a[q]);
+    for (int q = 0; q < E; q += 2) {
+      gated_step2<VEC, START>(Q, a + q, x + q);
+      gated_prod2<VEC, START>(P, a + q);
     }
     const int par = it & 1;
-    wsum[par][warp][lane] = make_float4(P[0], P[VEC - 1], Q[0], Q[VEC - 1]);
+    float4 front = make_float4(P[0], P[VEC - 1], Q[0], Q[VEC - 1]), own_warp;
+    gated_parts<VEC, START, true>(S, lane, front, own_warp);  // in the warp
+    wsum[par][warp][lane] = own_warp;
     __syncthreads();
-    // composition of the steps in front of this warp's; the last warp's, with its
-    // own, is the tile's
-    float4 front = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-    for (int w = 0; w < warp; ++w) gated_compose<VEC, START>(front, wsum[par][w][lane]);
-    if (warp == kGatedWarps - 1) {
-      float4 all = front;
-      gated_compose<VEC, START>(all, make_float4(P[0], P[VEC - 1], Q[0], Q[VEC - 1]));
-      if (C > 1)
-        for (int w = 0; w < C; ++w) st_peer(&csum[par][rank][lane], w, all);
-      else
-        csum[par][0][lane] = all;
-    }
-    gated_exchange(C, warp == kGatedWarps - 1);
     float hs[VEC];  // state in front of the warp's steps
-    for (int w = 0; w < C; ++w) {
-      if (w == rank) {
+    if (C == 1) {  // the warps' maps in order from the tile's start state
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) hs[e] = h[e];
+      for (int e = 0; e < VEC; ++e) hs[e] = h[e];
+#pragma unroll
+      for (int w = 0; w < kGatedWarps; ++w) {
+        gated_apply<VEC, START>(h, wsum[par][w][lane]);
+        if (w + 1 == warp) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) hs[e] = h[e];
+        }
       }
-      const float4 m = csum[par][w][lane];
-      h[0] = through<START>(m.x, h[0], m.z);
-      if constexpr (VEC == 2) h[1] = through<START>(m.y, h[1], m.w);
+    } else {
+      // composition of the warps in front of this one; the last warp's, with its
+      // own, is the tile's
+      float4 ahead = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+      for (int w = 0; w < warp; ++w) gated_compose<VEC, START>(ahead, wsum[par][w][lane]);
+      if (warp == kGatedWarps - 1) {
+        float4 all = ahead;
+        gated_compose<VEC, START>(all, own_warp);
+        for (int w = 0; w < C; ++w) st_peer(&csum[(par * C + rank) * 32 + lane], w, all);
+      }
+      gated_arrive(warp == kGatedWarps - 1);
+      cluster_wait();
+      for (int w = 0; w < C; ++w) {
+        if (w == rank) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) hs[e] = h[e];
+        }
+        gated_apply<VEC, START>(h, csum[(par * C + w) * 32 + lane]);
+      }
+      gated_apply<VEC, START>(hs, ahead);
     }
-    const int64_t tile = it * (int64_t)C + rank;
-    if (p.chunk_h && warp == 0 && tile < nT) {
-      const int64_t o = (i * nT + tile) * p.d + c, on = p.b * nT * p.d;
+    const int t_now = t_warp + it * tile_rows;
+    if (p.chunk_h && t_now % kGatedChunk == 0 && t_now < L && part == 0) {
+      const int64_t nC = (L + kGatedChunk - 1) / kGatedChunk;
+      const int64_t o = (i * nC + t_now / kGatedChunk) * p.d + c, on = p.b * nC * p.d;
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
         if (c + e < p.d && in_bounds(o + e, on, kBndChunk)) p.chunk_h[o + e] = hs[e];
     }
-    hs[0] = through<START>(front.x, hs[0], front.z);
-    if constexpr (VEC == 2) hs[1] = through<START>(front.y, hs[1], front.w);
+    if (S > 1) gated_apply<VEC, START>(hs, front);
     // replay
 #pragma unroll
-    for (int q = 0; q < E; ++q) {
-      hs[q % VEC] = through<START>(a[q], hs[q % VEC], x[q]);
-      x[q] = hs[q % VEC];
+    for (int q = 0; q < E; q += VEC) {
+      if constexpr (VEC == 2)
+        gated_step2<VEC, START>(hs, a + q, x + q);
+      else
+        hs[0] = through<START>(a[q], hs[0], x[q]);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[q + e] = hs[e];
     }
     if constexpr (GATE) {
 #pragma unroll
       for (int q = 0; q < E / 2; ++q) {
         const float2 o = mul2(make_float2(x[2 * q], x[2 * q + 1]),
-                              silu_2(staged_pair<T>(s + 3 * kGatedStage, q, lane)));
+                              silu_2(staged_pair<T>(s + 3 * kRows, q, lane)));
         x[2 * q] = o.x, x[2 * q + 1] = o.y;
       }
     }
-    const int64_t row = row0 + it * tile_rows;
-    if (n == kGatedSteps) {
+    if (n == STEPS) {
 #pragma unroll
-      for (int t = 0; t < kGatedSteps; ++t)
-        store_step<T, ASYNC>(p.y, p.y_ld, row + t, c, p.d, xy, x + t * VEC);
+      for (int t = 0; t < STEPS; ++t) dy.store(t, left, x + t * VEC);
     } else {
 #pragma unroll
-      for (int t = 0; t < kGatedSteps; ++t)
-        if (t < n) store_step<T, ASYNC>(p.y, p.y_ld, row + t, c, p.d, xy, x + t * VEC);
+      for (int t = 0; t < STEPS; ++t)
+        if (t < n) dy.store(t, left, x + t * VEC);
     }
+    dy.p += dy.step;
   }
-  if (p.h_last && rank == 0 && warp == 0) {
+  if (p.h_last && rank == 0 && warp == 0 && part == 0) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
       if (c + e < p.d && in_bounds(i * p.d + c + e, p.b * p.d, kBndState))
@@ -434,37 +544,48 @@ __global__ void __launch_bounds__(kGatedThreads, 3) gated_fwd_kernel(const Gated
 // below), two more with z.  a, f, a^2 / f, g and the adjoint stay in registers; r
 // is put back over the staged gates it came from.
 template <typename T, bool ASYNC, bool GATE, bool START>
-__global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const GatedBwdParams q_) {
+__global__ void __launch_bounds__(kGatedThreads, SSM_GB) gated_bwd_kernel(const GatedBwdParams q_) {
   const GatedParams &p = q_.f;
-  constexpr int VEC = gated_vec<T>(), E = kGatedSteps * VEC, NT = GATE ? 5 : 4;
+  constexpr int STEPS = kGatedBwdSteps, VEC = gated_vec<T>(), E = STEPS * VEC, NT = GATE ? 5 : 4;
+  constexpr int kRows = STEPS * kGatedRowBytes;  // bytes of a tensor's rows for a warp
   extern __shared__ __align__(16) char stage[];
   __shared__ float4 wsum[2][kGatedWarps][32];       // (P, mu) of the warps' steps
   __shared__ float2 wfwd[2][kGatedWarps][32];       // Q of the forward recurrence
-  __shared__ float4 csum[2][kGatedMaxCluster][32];  // (P, mu) of the cluster's tiles
+  float4 *const csum =
+      reinterpret_cast<float4 *>(stage + kGatedStages * gated_stage(NT, STEPS));  // [2][C][32]
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int C = p.csize, rank = (int)(blockIdx.x % (unsigned)C);
   const unsigned grp = blockIdx.x / (unsigned)C;
-  const int64_t c0 = (grp % (unsigned)p.ctiles) * (int64_t)(32 * VEC), i = grp / (unsigned)p.ctiles;
-  const int64_t c = c0 + lane * VEC;
-  const int64_t R = p.b * p.L, nT = (p.L + kGatedChunk - 1) / kGatedChunk;
-  const int iters = (int)((nT + C - 1) / C);
-  char *mine = stage + warp * NT * kGatedStage;
-  constexpr int kHalf = NT * kGatedWarps * kGatedStage;
+  const int S = p.parts, lc = 32 / S, part = lane / lc;
+  const int64_t c0 = (grp % (unsigned)p.ctiles) * (int64_t)(lc * VEC), i = grp / (unsigned)p.ctiles;
+  const int64_t c = c0 + lane % lc * VEC;
+  const int64_t R = p.b * p.L;
+  const int L = (int)p.L, own_rows = S * kGatedWarps * STEPS;  // of a tile
+  const int nT = (L + own_rows - 1) / own_rows;
+  const int iters = (nT + C - 1) / C;
+  char *mine = stage + warp * NT * kRows;
+  constexpr int kHalf = gated_stage(NT, STEPS);
   const GatedLane k = gated_lane<VEC>(p, c);
   // tiles from the end: rank 0 takes the last of the cluster's
-  const int64_t tile0 = nT - 1 - rank;
-  const int64_t t_first = tile0 * kGatedChunk + warp * kGatedSteps;  // the warp's first step
-  const int64_t row0 = i * p.L + t_first;
-  const int64_t tile_rows = -(int64_t)C * kGatedChunk;
-  GatedSrc<T, ASYNC> su, s_a, sg, so, sz;
-  su.init(p.u, p.u_ld, row0, tile_rows, c0, lane, R, p.d);
-  s_a.init(p.ga, p.ga_ld, row0, tile_rows, c0, lane, R, p.d);
-  sg.init(p.gx, p.gx_ld, row0, tile_rows, c0, lane, R, p.d);
-  so.init(q_.dout, q_.dout_ld, row0, tile_rows, c0, lane, R, p.d);
-  if constexpr (GATE) sz.init(p.z, p.z_ld, row0, tile_rows, c0, lane, R, p.d);
-  const int piece = gated_piece<T, ASYNC>(c0, lane, p.d);
-  const int64_t yu = extent(R, p.d, q_.du_ld), ya = extent(R, p.d, q_.dga_ld), yg = extent(R, p.d, q_.dgx_ld),
-                yz = extent(R, p.d, q_.dz_ld);
+  const int tile0 = nT - 1 - rank;
+  const int tile_rows = -C * own_rows;
+  // the warp's first step, the lane's, and that of the part it copies for
+  const int t_warp = tile0 * own_rows + warp * (S * STEPS);
+  const int t_lane = t_warp + part * STEPS;
+  const int t_copy = ASYNC ? t_warp + lane % 8 / (8 / S) * STEPS : t_lane;
+  GatedSrc<T, ASYNC, STEPS> su, s_a, sg, so, sz;
+  su.init(p.u, p.u_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
+  s_a.init(p.ga, p.ga_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
+  sg.init(p.gx, p.gx_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
+  so.init(q_.dout, q_.dout_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
+  if constexpr (GATE) sz.init(p.z, p.z_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
+  const int piece = gated_piece<T, ASYNC>(c0, lane, p.d, S);
+  GatedDst<T, ASYNC> du_, da_, dg_, dz_;
+  du_.init(q_.du, q_.du_ld, i * p.L + t_lane, tile_rows, c, R, p.d);
+  da_.init(q_.dga, q_.dga_ld, i * p.L + t_lane, tile_rows, c, R, p.d);
+  dg_.init(q_.dgx, q_.dgx_ld, i * p.L + t_lane, tile_rows, c, R, p.d);
+  if constexpr (GATE) dz_.init(q_.dz, q_.dz_ld, i * p.L + t_lane, tile_rows, c, R, p.d);
+  const int left = (int)(p.d - c < VEC ? p.d - c : VEC);  // channels in front of d
   float mu[VEC];                          // adjoint behind the cluster's next tiles
   float2 sA = f2(0.0f), sa = sA, sx = sA;  // sums of dl r, dgate_a / A, dgate_x
 #pragma unroll
@@ -474,30 +595,32 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
       mu[e] = q_.dh_last[i * p.d + c + e];
   }
   unsigned flag = 0;
-  float hnext[VEC];  // the next tile's start state
+  float hnext[VEC];  // state in front of the warp's next chunk
 #pragma unroll
   for (int e = 0; e < VEC; ++e) hnext[e] = 0.0f;
-  const auto rows_of = [&](int it) {
-    if (tile0 - it * (int64_t)C < 0) return 0;
-    const int64_t left = p.L - t_first - it * tile_rows;
-    return left >= kGatedSteps ? kGatedSteps : left > 0 ? (int)left : 0;
+  const auto rows_of = [&](int t, int it) {
+    if (tile0 - it * C < 0) return 0;
+    const int left = L - t - it * tile_rows;
+    return left >= STEPS ? STEPS : left > 0 ? left : 0;
   };
   const auto fetch = [&](int it) {
     if (it < iters) {
-      const int n = rows_of(it);
+      const int n = rows_of(t_copy, it);
       char *s = mine + (it & 1) * kHalf;
       su.fetch(s, n, piece, lane);
-      s_a.fetch(s + kGatedStage, n, piece, lane);
-      sg.fetch(s + 2 * kGatedStage, n, piece, lane);
-      so.fetch(s + 3 * kGatedStage, n, piece, lane);
-      if constexpr (GATE) sz.fetch(s + 4 * kGatedStage, n, piece, lane);
+      s_a.fetch(s + kRows, n, piece, lane);
+      sg.fetch(s + 2 * kRows, n, piece, lane);
+      so.fetch(s + 3 * kRows, n, piece, lane);
+      if constexpr (GATE) sz.fetch(s + 4 * kRows, n, piece, lane);
       if (START) {
-        const int64_t r = row0 + it * tile_rows + lane;
-        flag = lane < n && in_bounds(r, R, kBndAct) ? p.start[r] : 0;
+        const int t = t_warp + it * tile_rows + lane;
+        const int64_t r = i * p.L + t;
+        flag = lane < S * STEPS && t >= 0 && t < L && in_bounds(r, R, kBndAct) ? p.start[r] : 0;
       }
-      const int64_t tile = tile0 - it * (int64_t)C;
-      if (tile >= 0) {
-        const int64_t o = (i * nT + tile) * p.d + c, on = p.b * nT * p.d;
+      const int t_now = t_warp + it * tile_rows;
+      if (t_now >= 0 && t_now < L) {  // state in front of the warp's chunk
+        const int64_t nC = (L + kGatedChunk - 1) / kGatedChunk;
+      const int64_t o = (i * nC + t_now / kGatedChunk) * p.d + c, on = p.b * nC * p.d;
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
           if (c + e < p.d && in_bounds(o + e, on, kBndChunk)) hnext[e] = __ldg(p.chunk_h + o + e);
@@ -511,22 +634,22 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
   }
   fetch(0);
   for (int it = 0; it < iters; ++it) {
-    const unsigned bits = START ? __ballot_sync(~0u, flag != 0) : 0;
-    float hs[VEC];  // state in front of the tile, then of the warp's steps
+    const unsigned bits = START ? __ballot_sync(~0u, flag != 0) >> (part * STEPS) & ((1u << STEPS) - 1) : 0;
+    const bool any = START && __any_sync(~0u, bits != 0);
+    float hs[VEC];  // state in front of the chunk, then of the lane's steps
 #pragma unroll
     for (int e = 0; e < VEC; ++e) hs[e] = hnext[e];
     __syncwarp();
     fetch(it + 1);
     cp_async_wait<1>();
     __syncwarp();
-    const int64_t row = row0 + it * tile_rows;
-    const int n = rows_of(it);
+    const int n = rows_of(t_lane, it);
     char *s = mine + (it & 1) * kHalf;
     float a[E], f[E], af[E], g[E], lam[E];  // af = a^2 / f; lam: dout silu(z), later the adjoint
 #pragma unroll
     for (int q = 0; q < E / 2; ++q) {
-      float2 er = ex2_2(fma2(staged_pair<T>(s + kGatedStage, q, lane), f2(-kLog2e), k.na));
-      float2 eg = ex2_2(fma2(staged_pair<T>(s + 2 * kGatedStage, q, lane), f2(-kLog2e), k.nx));
+      float2 er = ex2_2(fma2(staged_pair<T>(s + kRows, q, lane), f2(-kLog2e), k.na));
+      float2 eg = ex2_2(fma2(staged_pair<T>(s + 2 * kRows, q, lane), f2(-kLog2e), k.nx));
       constexpr float kCap = 1152921504606846976.0f;  // 2^60
       er = __fadd2_rn(make_float2(min_nan(er.x, kCap), min_nan(er.y, kCap)), f2(1.0f));
       eg = __fadd2_rn(make_float2(min_nan(eg.x, kCap), min_nan(eg.y, kCap)), f2(1.0f));
@@ -537,14 +660,14 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
       float2 rho = rsqrt_2(w);
       float2 fv = mul2(w, rho);
       rho = make_float2(w.x == kDecayMinW ? 0.0f : rho.x, w.y == kDecayMinW ? 0.0f : rho.y);
-      if (START && bits) {
+      if (START && any) {
         const int s0 = 2 * q / VEC, s1 = (2 * q + 1) / VEC;
         if (bits >> s0 & 1) av.x = 0.0f, fv.x = 1.0f, rho.x = 0.0f;
         if (bits >> s1 & 1) av.y = 0.0f, fv.y = 1.0f, rho.y = 0.0f;
       }
       const float2 afv = mul2(mul2(av, av), rho);
-      float2 go = staged_pair<T>(s + 3 * kGatedStage, q, lane);
-      if constexpr (GATE) go = mul2(go, silu_2(staged_pair<T>(s + 4 * kGatedStage, q, lane)));
+      float2 go = staged_pair<T>(s + 3 * kRows, q, lane);
+      if constexpr (GATE) go = mul2(go, silu_2(staged_pair<T>(s + 4 * kRows, q, lane)));
       a[2 * q] = av.x, a[2 * q + 1] = av.y;
       f[2 * q] = fv.x, f[2 * q + 1] = fv.y;
       af[2 * q] = afv.x, af[2 * q + 1] = afv.y;
@@ -552,15 +675,15 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
       lam[2 * q] = go.x, lam[2 * q + 1] = go.y;
       // r over the gates it came from
       if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<float *>(s + kGatedStage + q * kGatedRowBytes + lane * 4) = r.x;
-        *reinterpret_cast<float *>(s + 2 * kGatedStage + q * kGatedRowBytes + lane * 4) = r.y;
+        *reinterpret_cast<float *>(s + kRows + q * kGatedRowBytes + lane * 4) = r.x;
+        *reinterpret_cast<float *>(s + 2 * kRows + q * kGatedRowBytes + lane * 4) = r.y;
       } else {
-        float *o = reinterpret_cast<float *>(s + kGatedStage) + lane;
+        float *o = reinterpret_cast<float *>(s + kRows) + lane;
         o[2 * q * 32] = r.x;
         o[(2 * q + 1) * 32] = r.y;
       }
     }
-    if (n < kGatedSteps) {
+    if (n < STEPS) {
 #pragma unroll
       for (int q = 0; q < E; ++q)
         if (q / VEC >= n) a[q] = 1.0f, f[q] = 0.0f, lam[q] = 0.0f;
@@ -572,11 +695,9 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
     for (int q = 0; q < E / 2; ++q) {
       const float2 u = staged_pair<T>(s, q, lane);
       const float2 x = mul2(mul2(make_float2(f[2 * q], f[2 * q + 1]), make_float2(g[2 * q], g[2 * q + 1])), u);
-      const int e0 = (2 * q) % VEC, e1 = (2 * q + 1) % VEC;
-      Q[e0] = through<START>(a[2 * q], Q[e0], x.x);
-      Q[e1] = through<START>(a[2 * q + 1], Q[e1], x.y);
-      P[e0] = times<START>(P[e0], a[2 * q]);
-      P[e1] = times<START>(P[e1], a[2 * q + 1]);
+      const float xv[2] = {x.x, x.y};
+      gated_step2<VEC, START>(Q, a + 2 * q, xv);
+      gated_prod2<VEC, START>(P, a + 2 * q);
     }
     // mu_t = a_t (go_t + mu_{t+1}); a step that starts a sequence hands nothing back
 #pragma unroll
@@ -585,39 +706,55 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
       M[q % VEC] = START && a[q] == 0.0f ? 0.0f : m;
     }
     const int par = it & 1;
-    wsum[par][warp][lane] = make_float4(P[0], P[VEC - 1], M[0], M[VEC - 1]);
-    wfwd[par][warp][lane] = make_float2(Q[0], Q[VEC - 1]);
+    // in the warp: back, what lies behind the lane's steps; ahead, in front of them
+    float4 back = make_float4(P[0], P[VEC - 1], M[0], M[VEC - 1]), own_warp;
+    float4 ahead = make_float4(P[0], P[VEC - 1], Q[0], Q[VEC - 1]), fwd_warp;
+    gated_parts<VEC, START, false>(S, lane, back, own_warp);
+    gated_parts<VEC, START, true>(S, lane, ahead, fwd_warp);
+    wsum[par][warp][lane] = own_warp;
+    wfwd[par][warp][lane] = make_float2(fwd_warp.z, fwd_warp.w);
     __syncthreads();
-    // the steps behind this warp's; the first warp's, with its own, is the tile's
-    float4 back = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-    for (int w = kGatedWarps - 1; w > warp; --w) gated_compose<VEC, START>(back, wsum[par][w][lane]);
-    if (warp == 0) {
-      float4 all = back;
-      gated_compose<VEC, START>(all, make_float4(P[0], P[VEC - 1], M[0], M[VEC - 1]));
-      if (C > 1)
-        for (int w = 0; w < C; ++w) st_peer(&csum[par][rank][lane], w, all);
-      else
-        csum[par][0][lane] = all;
-    }
-    for (int w = 0; w < warp; ++w) {
+    // from the chunk's start state, through its warps in front of this one
+    const int first = warp - warp % (kGatedWarps / S);  // of the chunk
+    for (int w = first; w < warp; ++w) {
       const float4 m = wsum[par][w][lane];
       const float2 x = wfwd[par][w][lane];
-      hs[0] = through<START>(m.x, hs[0], x.x);
-      if constexpr (VEC == 2) hs[1] = through<START>(m.y, hs[1], x.y);
+      gated_apply<VEC, START>(hs, make_float4(m.x, m.y, x.x, x.y));
     }
-    gated_exchange(C, warp == 0);
+    if (S > 1) gated_apply<VEC, START>(hs, ahead);
     float mb[VEC];  // adjoint behind the warp's steps
-    for (int w = 0; w < C; ++w) {
-      if (w == rank) {
+    if (C == 1) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) mb[e] = mu[e];
+      for (int e = 0; e < VEC; ++e) mb[e] = mu[e];
+#pragma unroll
+      for (int w = kGatedWarps - 1; w >= 0; --w) {
+        gated_apply<VEC, START>(mu, wsum[par][w][lane]);
+        if (w - 1 == warp) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) mb[e] = mu[e];
+        }
       }
-      const float4 m = csum[par][w][lane];
-      mu[0] = through<START>(m.x, mu[0], m.z);
-      if constexpr (VEC == 2) mu[1] = through<START>(m.y, mu[1], m.w);
+    } else {
+      // the warps behind this one; the first warp's, with its own, is the tile's
+      float4 behind = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+      for (int w = kGatedWarps - 1; w > warp; --w) gated_compose<VEC, START>(behind, wsum[par][w][lane]);
+      if (warp == 0) {
+        float4 all = behind;
+        gated_compose<VEC, START>(all, own_warp);
+        for (int w = 0; w < C; ++w) st_peer(&csum[(par * C + rank) * 32 + lane], w, all);
+      }
+      gated_arrive(warp == 0);
+      cluster_wait();
+      for (int w = 0; w < C; ++w) {
+        if (w == rank) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) mb[e] = mu[e];
+        }
+        gated_apply<VEC, START>(mu, csum[(par * C + w) * 32 + lane]);
+      }
+      gated_apply<VEC, START>(mb, behind);
     }
-    mb[0] = through<START>(back.x, mb[0], back.z);
-    if constexpr (VEC == 2) mb[1] = through<START>(back.y, mb[1], back.w);
+    if (S > 1) gated_apply<VEC, START>(mb, back);
     // the adjoints, last step first
 #pragma unroll
     for (int q = E - 1; q >= 0; --q) {
@@ -633,10 +770,10 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
       const float2 gv = make_float2(g[2 * q], g[2 * q + 1]), lv = make_float2(lam[2 * q], lam[2 * q + 1]);
       float2 r;
       if constexpr (sizeof(T) == 2) {
-        r.x = *reinterpret_cast<const float *>(s + kGatedStage + q * kGatedRowBytes + lane * 4);
-        r.y = *reinterpret_cast<const float *>(s + 2 * kGatedStage + q * kGatedRowBytes + lane * 4);
+        r.x = *reinterpret_cast<const float *>(s + kRows + q * kGatedRowBytes + lane * 4);
+        r.y = *reinterpret_cast<const float *>(s + 2 * kRows + q * kGatedRowBytes + lane * 4);
       } else {
-        r = staged_pair<float>(s + kGatedStage, q, lane);
+        r = staged_pair<float>(s + kRows, q, lane);
       }
       const float2 gu = mul2(gv, u), x = mul2(fv, gu);
       const int e0 = (2 * q) % VEC, e1 = (2 * q + 1) % VEC;
@@ -656,7 +793,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
       const float2 dlr = mul2(dl, r);
       float2 dga = mul2(dlr, __ffma2_rn(r, f2(-1.0f), f2(1.0f)));
       const bool on0 = (2 * q) / VEC < n, on1 = (2 * q + 1) / VEC < n;
-      if (n == kGatedSteps) {
+      if (n == STEPS) {
         sA = __fadd2_rn(sA, dlr);
         sa = __fadd2_rn(sa, dga);
         sx = __fadd2_rn(sx, dgx);
@@ -668,8 +805,8 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
       const float vu[2] = {du.x, du.y}, va[2] = {dga.x, dga.y}, vg[2] = {dgx.x, dgx.y};
       float vz[2];
       if constexpr (GATE) {
-        const float2 dy = staged_pair<T>(s + 3 * kGatedStage, q, lane);
-        const float2 z = staged_pair<T>(s + 4 * kGatedStage, q, lane);
+        const float2 dy = staged_pair<T>(s + 3 * kRows, q, lane);
+        const float2 z = staged_pair<T>(s + 4 * kRows, q, lane);
         const float2 sg = rcp_2(__fadd2_rn(ex2_2(mul2(z, f2(-kLog2e))), f2(1.0f)));
         // silu'(z) = s + z s (1 - s)
         const float2 ds = __ffma2_rn(mul2(z, sg), __ffma2_rn(sg, f2(-1.0f), f2(1.0f)), sg);
@@ -680,20 +817,24 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
       for (int e = 0; e < 2; e += VEC) {
         const int t = (2 * q + e) / VEC;
         if (t >= n) continue;
-        store_step<T, ASYNC>(q_.du, q_.du_ld, row + t, c, p.d, yu, vu + e);
-        store_step<T, ASYNC>(q_.dga, q_.dga_ld, row + t, c, p.d, ya, va + e);
-        store_step<T, ASYNC>(q_.dgx, q_.dgx_ld, row + t, c, p.d, yg, vg + e);
-        if constexpr (GATE) store_step<T, ASYNC>(q_.dz, q_.dz_ld, row + t, c, p.d, yz, vz + e);
+        du_.store(t, left, vu + e);
+        da_.store(t, left, va + e);
+        dg_.store(t, left, vg + e);
+        if constexpr (GATE) dz_.store(t, left, vz + e);
       }
     }
+    du_.p += du_.step;
+    da_.p += da_.step;
+    dg_.p += dg_.step;
+    if constexpr (GATE) dz_.p += dz_.step;
   }
-  if (q_.dh0 && rank == 0 && warp == 0) {
+  if (q_.dh0 && rank == 0 && warp == 0 && part == 0) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
       if (c + e < p.d && in_bounds(i * p.d + c + e, p.b * p.d, kBndState))
         q_.dh0[i * p.d + c + e] = mu[e];
   }
-  // the parameters' sums over the CTA's warps
+  // the parameters' sums over the CTA's warps and their parts
   if constexpr (VEC == 1) {  // a pair holds two steps of one channel
     sA.x += sA.y, sa.x += sa.y, sx.x += sx.y;
   }
@@ -704,10 +845,10 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(const Gated
   red[(1 * kGatedWarps + warp) * 32 + lane] = mul2(sa, mul2(k.A2, f2(kLn2)));
   red[(2 * kGatedWarps + warp) * 32 + lane] = sx;
   __syncthreads();
-  if (warp < 3) {
-    float2 t = red[warp * kGatedWarps * 32 + lane];
-#pragma unroll
-    for (int w = 1; w < kGatedWarps; ++w) t = __fadd2_rn(t, red[(warp * kGatedWarps + w) * 32 + lane]);
+  if (warp < 3 && part == 0) {
+    float2 t = f2(0.0f);
+    for (int w = 0; w < kGatedWarps; ++w)
+      for (int s = 0; s < S; ++s) t = __fadd2_rn(t, red[(warp * kGatedWarps + w) * 32 + s * lc + lane]);
     const int64_t o = ((i * C + rank) * 3 + warp) * p.d + c, on = p.b * C * 3 * p.d;
     if (c < p.d && in_bounds(o, on, kBndWork)) q_.part[o] = t.x;
     if constexpr (VEC == 2)
@@ -737,7 +878,7 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const GatedParams p, fl
     const float r = sigmoid_f32(ga[e] + (p.ba ? ld_param(p.ba, c + e, p.d) : 0.0f));
     const float g = sigmoid_f32(gx[e] + (p.bx ? ld_param(p.bx, c + e, p.d) : 0.0f));
     float2 a, w;
-    decay2(f2(min_nan(ld_param(p.A, c + e, p.d) * kLog2e, 126.0f) * r), a, w);
+    decay2(f2(ld_param(p.A, c + e, p.d) * kLog2e * r), a, w);
     h[e] = fmaf(a.x, h[e], w.x * rsqrt_approx(w.x) * (g * u[e]));
     y[e] = h[e];
     if constexpr (GATE) y[e] *= silu_f32(z[e]);

@@ -142,8 +142,8 @@ def test_refusals(k):
 
 
 def test_size_queries():
-    assert S.ssm_gated_scan_states_bytes(2, 64, 8) == 2 * 8 * 4
-    assert S.ssm_gated_scan_states_bytes(2, 65, 8) == 2 * 2 * 8 * 4
+    assert S.ssm_gated_scan_states_bytes(2, 32, 8) == 2 * 8 * 4
+    assert S.ssm_gated_scan_states_bytes(2, 33, 8) == 2 * 2 * 8 * 4
     assert S.ssm_gated_scan_states_bytes(2, 0, 8) == 0
     for q in (L.ssm_gated_scan_states_bytes(-1, 2, 3), L.ssm_gated_scan_bwd_workspace_bytes(1, -2, 3),
               L.ssm_conv1d_bwd_workspace_bytes(1, 2, 3, 9), L.ssm_conv1d_bwd_workspace_bytes(1, 2, 3, 0),
