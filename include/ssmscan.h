@@ -488,7 +488,7 @@ ssm_status ss2d_cross_merge(const void *ys, void *y, int64_t b, int64_t H,
  *
  * Rows with a stride: every activation of these calls has its own row stride
  * NAME_ld, in elements: row r (of b * L, of b, or of `rows`) starts at
- * NAME + r * NAME_ld, its channels are adjacent, and NAME_ld >= channels.  So
+ * NAME + r * NAME_ld, its channels are adjacent, channels <= NAME_ld < 2^31.  So
  * x and z may be the two halves of one projection's rows, and their gradients
  * the two halves of one buffer.  Rows of outputs may interleave with rows of
  * other arguments of the same stride, but share no element with them.  States,

@@ -51,6 +51,8 @@ class Args {
     if (status_ == SSM_OK && !aligned(p, es))
       status_ = fail(SSM_ERR_INVALID_ARG, "%s: %s is not %zu-byte aligned", what_, name, es);
     int64_t t;
+    if (status_ == SSM_OK && ld >= (int64_t)1 << 31)
+      status_ = fail(SSM_ERR_INVALID_ARG, "%s: %s_ld %lld is not below 2^31", what_, name, (long long)ld);
     if (status_ == SSM_OK && ld < d)
       status_ = fail(SSM_ERR_INVALID_ARG, "%s: %s_ld %lld is below the row's %lld elements", what_,
                      name, (long long)ld, (long long)d);
@@ -156,6 +158,10 @@ ssm_status pass_state(const float *src, float *dst, int64_t n, cudaStream_t st, 
   return check_launch(what);
 }
 
+// A row stride as the gated kernels take it; -1, which the argument check
+// refuses (as below the row), where it is not below 2^31.
+int ld32(int64_t ld) { return ld >= 0 && ld <= 0x7fffffff ? (int)ld : -1; }
+
 constexpr int64_t kMaxGrid = 0x7fffffff;
 
 // Whether rows of T can be read VEC elements at a time.
@@ -170,37 +176,37 @@ bool vec_rows(int64_t vec, size_t es, int64_t d, std::initializer_list<std::pair
 int64_t gated_chunks(int64_t L) { return (L + ssm::kGatedChunk - 1) / ssm::kGatedChunk; }
 
 // Parts of a warp (S) and CTAs of a cluster (C).  A CTA's round is 64 S steps of
-// 1 / S of the channels, the same work whatever S; an SM's time goes as the rounds
-// of a CTA times the CTAs it holds, or times two where it holds fewer (a round's
-// own latency), a quarter more with clusters, whose CTAs wait for each other in
-// every round.  Of equal ones the one with the widest rows.  Measured (B200, bf16, b
-// = 8, L = 2048, d = 1536, forward, us): see gated_scan.cuh.
+// 1 / S of the channels, the same work whatever S.  In tenths of a microsecond, as
+// measured (forward; the backward goes alike): a round takes 14 with one CTA on an
+// SM, 24 with as many as it holds (2 of bf16, 3 of fp32); clusters, whose CTAs wait
+// for each other in every round, take a third more; a CTA of 32 bytes of a row (S =
+// 4) a fifth more than one of 64, one of 128 a tenth less.  bf16, b = 8, L = 2048, d
+// = 1536 (us): S = 2 61, S = 1 70, S = 4 70, S = 1 in clusters of 2 81; b = 1, L =
+// 16384, d = 2560: S = 1 in clusters of 8 and S = 2 alone differ 1.3 times.
 struct GatedPlan {
   int parts, ctiles, csize;
 };
-GatedPlan gated_plan(int64_t b, int64_t L, int64_t d, int channels) {
-  const int64_t sms = device_sms();
+GatedPlan gated_plan(int64_t b, int64_t L, int64_t d, size_t es) {
+  const int64_t sms = device_sms(), holds = es == 2 ? 2 : 3;
   GatedPlan best{1, 1, 1};
   int64_t least = -1;
   for (int s = 1; s <= 4; s *= 2)
     for (int c = 1; c <= ssm::kGatedMaxCluster; c *= 2) {
-      const int64_t tiles = (d + channels / s - 1) / (channels / s);
+      const int64_t channels = 128 / (int64_t)es / s;
+      const int64_t tiles = (d + channels - 1) / channels, ctas = b * tiles * c;
       const int64_t rounds = (L + 64 * s * c - 1) / (64 * s * c);
-      const int64_t held = (b * tiles * c + sms - 1) / sms;
-      const int64_t cost = rounds * (held > 2 ? held : 2) * (c > 1 ? 5 : 4);
+      const int64_t waves = ctas / (holds * sms), rest = ctas % (holds * sms);
+      const int64_t wave = waves * 24 + (rest == 0 ? 0 : 14 + 10 * ((rest + sms - 1) / sms - 1) / (holds - 1));
+      const int64_t cost = rounds * wave * (c > 1 ? 4 : 3) * (s == 1 ? 9 : s == 2 ? 10 : 12);
       if (least < 0 || cost < least) {
         least = cost;
         best = GatedPlan{s, (int)tiles, c};
       }
     }
-#ifdef SSM_GS
-  best.parts = SSM_GS, best.csize = SSM_GC;
-  best.ctiles = (int)((d + channels / SSM_GS - 1) / (channels / SSM_GS));
-#endif
   return best;
 }
 int64_t gated_bwd_parts(int64_t b, int64_t L, int64_t d) {  // of whichever type
-  const int f = gated_plan(b, L, d, 32).csize, h = gated_plan(b, L, d, 64).csize;
+  const int f = gated_plan(b, L, d, 4).csize, h = gated_plan(b, L, d, 2).csize;
   return b * (f > h ? f : h);
 }
 
@@ -232,7 +238,7 @@ ssm_status launch_gated(const P &p, int64_t b, const GatedPlan &g, int smem, int
 
 template <typename T, bool ASYNC, bool GATE>
 ssm_status gated_fwd_t(ssm::GatedParams p, cudaStream_t st) {
-  const GatedPlan g = gated_plan(p.b, p.L, p.d, 32 * ssm::gated_vec<T>());
+  const GatedPlan g = gated_plan(p.b, p.L, p.d, sizeof(T));
   p.parts = g.parts, p.ctiles = g.ctiles, p.csize = g.csize;
   const int smem = ssm::gated_smem(GATE ? 4 : 3, ssm::kGatedFwdSteps, g.csize);
   constexpr int most = ssm::gated_smem(GATE ? 4 : 3, ssm::kGatedFwdSteps, ssm::kGatedMaxCluster);
@@ -242,7 +248,7 @@ ssm_status gated_fwd_t(ssm::GatedParams p, cudaStream_t st) {
 }
 template <typename T, bool ASYNC, bool GATE>
 ssm_status gated_bwd_t(ssm::GatedBwdParams q, int64_t *parts, cudaStream_t st) {
-  const GatedPlan g = gated_plan(q.f.b, q.f.L, q.f.d, 32 * ssm::gated_vec<T>());
+  const GatedPlan g = gated_plan(q.f.b, q.f.L, q.f.d, sizeof(T));
   q.f.parts = g.parts, q.f.ctiles = g.ctiles, q.f.csize = g.csize;
   *parts = q.f.b * g.csize;
   const int smem = ssm::gated_smem(GATE ? 5 : 4, ssm::kGatedBwdSteps, g.csize);
@@ -740,8 +746,8 @@ ssm_status ssm_gated_scan_fwd(const void *u, int64_t u_ld, const void *gate_a, i
                               ssm_dtype dtype, ssm_stream_t stream) {
   const char *what = "ssm_gated_scan_fwd";
   g_last_error.clear();
-  ssm::GatedParams p{u,  gate_a, gate_x, z,      u_ld,         gate_a_ld, gate_x_ld, z_ld, A, bias_a,
-                     bias_x, seq_start, h0, h_last, y, y_ld, chunk_states, b, L, d_in};
+  ssm::GatedParams p{u, gate_a, gate_x, z, ld32(u_ld), ld32(gate_a_ld), ld32(gate_x_ld), ld32(z_ld), A,
+                     bias_a, bias_x, seq_start, h0, h_last, y, ld32(y_ld), chunk_states, b, L, d_in};
   Args a(what, esize(dtype));
   if (ssm_status s = check_gated(what, a, p, dtype)) return s;
   if (b * L > 0 && d_in > 0 && !y) return fail(SSM_ERR_INVALID_ARG, "%s: y is required", what);
@@ -778,9 +784,9 @@ ssm_status ssm_gated_scan_bwd(const void *u, int64_t u_ld, const void *gate_a, i
   const char *what = "ssm_gated_scan_bwd";
   g_last_error.clear();
   if (!z) dz = nullptr;
-  ssm::GatedParams f{u,  gate_a, gate_x, z, u_ld, gate_a_ld, gate_x_ld, z_ld, A, bias_a, bias_x,
-                     seq_start, nullptr, nullptr, nullptr, 0, const_cast<float *>(chunk_states), b,
-                     L, d_in};
+  ssm::GatedParams f{u, gate_a, gate_x, z, ld32(u_ld), ld32(gate_a_ld), ld32(gate_x_ld), ld32(z_ld), A,
+                     bias_a, bias_x, seq_start, nullptr, nullptr, nullptr, 0,
+                     const_cast<float *>(chunk_states), b, L, d_in};
   Args a(what, esize(dtype));
   if (ssm_status s = check_gated(what, a, f, dtype)) return s;
   const int64_t R = b * L;
@@ -813,8 +819,8 @@ ssm_status ssm_gated_scan_bwd(const void *u, int64_t u_ld, const void *gate_a, i
   if (ssm_status s = check_states(what, chunk_states, chunk_states_bytes, b, L, d_in)) return s;
   if (ssm_status s = need_workspace(what, workspace, workspace_bytes, need)) return s;
   float *part = static_cast<float *>(workspace);
-  ssm::GatedBwdParams q{f,  dout,  dout_ld, dh_last,    du,         dgate_a, dgate_x,
-                        dz, du_ld, dgate_a_ld, dgate_x_ld, dz_ld, dh0, part};
+  ssm::GatedBwdParams q{f,  dout, ld32(dout_ld), dh_last, du, dgate_a, dgate_x, dz, ld32(du_ld),
+                        ld32(dgate_a_ld), ld32(dgate_x_ld), ld32(dz_ld), dh0, part};
   int64_t parts = 0;
   if (ssm_status s = dtype == SSM_BF16 ? gated_bwd_any<__nv_bfloat16>(q, &parts, st)
                                        : gated_bwd_any<float>(q, &parts, st))
@@ -829,8 +835,8 @@ ssm_status ssm_gated_state_update(float *state, const void *u, int64_t u_ld, con
                                   int64_t d_in, ssm_dtype dtype, ssm_stream_t stream) {
   const char *what = "ssm_gated_state_update";
   g_last_error.clear();
-  ssm::GatedParams p{u,  gate_a, gate_x, z, u_ld, gate_a_ld, gate_x_ld, z_ld, A, bias_a, bias_x,
-                     nullptr, nullptr, nullptr, y, y_ld, nullptr, b, 1, d_in};
+  ssm::GatedParams p{u, gate_a, gate_x, z, ld32(u_ld), ld32(gate_a_ld), ld32(gate_x_ld), ld32(z_ld), A,
+                     bias_a, bias_x, nullptr, nullptr, nullptr, y, ld32(y_ld), nullptr, b, 1, d_in};
   Args a(what, esize(dtype));
   if (ssm_status s = check_gated(what, a, p, dtype)) return s;
   if (b > 0 && d_in > 0 && (!state || !y))

@@ -30,13 +30,13 @@ namespace ssm {
 
 struct GatedParams {
   const void *u, *ga, *gx, *z;
-  int64_t u_ld, ga_ld, gx_ld, z_ld;
+  int u_ld, ga_ld, gx_ld, z_ld;  // below 2^31: offsets of a few rows take one multiply
   const float *A, *ba, *bx;
   const uint8_t *start;
   const float *h0;
   float *h_last;
   void *y;
-  int64_t y_ld;
+  int y_ld;
   float *chunk_h;
   int64_t b, L, d;
   int parts;    // S: parts of a warp
@@ -47,28 +47,25 @@ struct GatedParams {
 struct GatedBwdParams {
   GatedParams f;  // inputs of the forward; chunk_h is read
   const void *dout;
-  int64_t dout_ld;
+  int dout_ld;
   const float *dh_last;
   void *du, *dga, *dgx, *dz;
-  int64_t du_ld, dga_ld, dgx_ld, dz_ld;
+  int du_ld, dga_ld, dgx_ld, dz_ld;
   float *dh0;
   float *part;  // (b * csize, 3, d): sums of dA, dbias_a, dbias_x
 };
 
 constexpr int kGatedWarps = 8;  // of a CTA
 constexpr int kGatedThreads = 32 * kGatedWarps;
-// Steps of a lane in a tile, and CTAs an SM holds.
-#ifndef SSM_GF
-#define SSM_GF 2
-#endif
-#ifndef SSM_GB
-#define SSM_GB 2
-#endif
-#ifndef SSM_GFS
-#define SSM_GFS 8
-#endif
-constexpr int kGatedFwdSteps = SSM_GFS, kGatedBwdSteps = 4;
-static_assert(kGatedWarps * kGatedBwdSteps == kGatedChunk && 2 * kGatedFwdSteps <= kGatedChunk,
+// Steps of a lane in a tile, and CTAs an SM holds (bf16 lanes take two channels:
+// 128 registers).  Measured (B200, b = 8, L = 2048, d = 1536, us): bf16 forward 8
+// steps with 2 CTAs 61, with 3 (spills) 64, 4 steps with 2, 3, 4 CTAs 76, 73, 79,
+// 16 steps 60 (86 with z, whose stages leave room for one CTA); backward 4 steps
+// with 2 CTAs 145, with 3 (spills) 179, 8 steps with 2 (spills) 178, with 1 168.
+// fp32 forward with 2, 3 CTAs 86, 78, backward 193, 189.
+constexpr int kGatedFwdSteps = 8, kGatedBwdSteps = 4;
+template <typename T> constexpr int gated_ctas() { return sizeof(T) == 2 ? 2 : 3; }
+static_assert(kGatedWarps * kGatedBwdSteps == kGatedChunk && 4 * kGatedFwdSteps <= kGatedChunk,
               "a backward tile is S chunks, a forward warp starts at most one");
 constexpr int kGatedMaxCluster = 8;
 constexpr int kGatedRowBytes = 128;
@@ -240,28 +237,26 @@ __device__ __forceinline__ GatedLane gated_lane(const GatedParams &p, int64_t c)
 // aligned, d a multiple of 16 bytes), lane l the 16 bytes l % 8 of steps l / 8 (and
 // l / 8 + 4); else element loads.  Rows past the end and channels past d become zeros.
 template <typename T, bool ASYNC, int STEPS> struct GatedSrc {
-  const char *p;      // the lane's first element of the next tile
-  int64_t ld, step;   // bytes
-  const char *lo, *hi;  // the buffer (debug-bounds build)
+  const char *p;        // the lane's first element of the next tile
+  const char *lo, *hi;  // the buffer (past-the-end pieces, debug-bounds build)
   // row: the warp's first
-  __device__ __forceinline__ void init(const void *src, int64_t ld_, int64_t row, int64_t tile_rows,
-                                       int64_t c0, int lane, int64_t rows, int64_t d, int S) {
-    ld = ld_ * (int64_t)sizeof(T);
-    step = tile_rows * ld;
+  __device__ __forceinline__ void init(const void *src, int ld, int64_t row, int64_t c0, int lane,
+                                       int64_t rows, int64_t d, int S) {
     lo = static_cast<const char *>(src);
-    hi = lo + extent(rows, d, ld_) * (int64_t)sizeof(T);
+    hi = lo + extent(rows, d, ld) * (int64_t)sizeof(T);
     const int lc = 32 / S, pc = 8 / S;  // lanes, 16-byte pieces of a part
-    p = lo + row * ld + c0 * (int64_t)sizeof(T) +
-        (ASYNC ? (lane % 8 / pc * STEPS + lane / 8) * ld + lane % 8 % pc * 16
-               : lane / lc * STEPS * ld + lane % lc * gated_vec<T>() * (int64_t)sizeof(T));
+    const int64_t r = row + (ASYNC ? lane % 8 / pc * STEPS + lane / 8 : lane / lc * STEPS);
+    p = lo + (r * ld + c0) * (int64_t)sizeof(T) +
+        (ASYNC ? lane % 8 % pc * 16 : lane % lc * gated_vec<T>() * (int)sizeof(T));
   }
   // n rows of this tile for the part whose bytes the lane copies; bytes: 16 where
-  // its piece lies in front of d, else 0 (elements: how many of the lane's do)
-  __device__ __forceinline__ void fetch(char *s, int n, int bytes, int lane) {
+  // its piece lies in front of d, else 0 (elements: how many of the lane's do);
+  // then on by tile_rows rows
+  __device__ __forceinline__ void fetch(char *s, int n, int bytes, int lane, int ld, int tile_rows) {
     if constexpr (ASYNC) {
 #pragma unroll
       for (int j = 0; j < STEPS / 4; ++j) {
-        const char *q = p + 4 * j * ld;
+        const char *q = p + (int64_t)ld * (4 * j * (int)sizeof(T));
         int b = bytes;
         if (n < STEPS && lane / 8 + 4 * j >= n) b = 0;
         if (b && !in_bounds(q - lo, hi - lo - 15, kBndAct)) b = 0;
@@ -275,7 +270,7 @@ template <typename T, bool ASYNC, int STEPS> struct GatedSrc {
       for (int r = 0; r < STEPS; ++r)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const char *q = p + r * ld + e * (int)sizeof(T);
+          const char *q = p + (int64_t)ld * (r * (int)sizeof(T)) + e * (int)sizeof(T);
           v[r][e] = r < n && e < bytes && in_bounds(q - lo, hi - lo, kBndAct)
                         ? *reinterpret_cast<const T *>(q) : T(0.0f);
         }
@@ -285,7 +280,7 @@ template <typename T, bool ASYNC, int STEPS> struct GatedSrc {
         for (int e = 0; e < VEC; ++e)
           reinterpret_cast<T *>(s + r * kGatedRowBytes)[lane * VEC + e] = v[r][e];
     }
-    p += step;
+    p += (int64_t)ld * (tile_rows * (int)sizeof(T));
   }
 };
 // The `bytes` of fetch for a lane.
@@ -309,25 +304,19 @@ __device__ __forceinline__ float2 staged_pair(const char *s, int k, int lane) {
   }
 }
 
-// An output's place: the lane's channels in the first of its steps of a tile,
-// `step` elements to the next tile's.
+// An output's place: the lane's channels in the first of its steps of a tile.
 template <typename T, bool ASYNC> struct GatedDst {
-  T *p;
-  int64_t ld, step;
-  T *lo;
+  T *p, *lo;
   int64_t n;  // elements of the buffer (debug-bounds build)
-  __device__ __forceinline__ void init(void *dst, int64_t ld_, int64_t row, int64_t tile_rows, int64_t c,
-                                       int64_t rows, int64_t d) {
+  __device__ __forceinline__ void init(void *dst, int ld, int64_t row, int64_t c, int64_t rows, int64_t d) {
     lo = static_cast<T *>(dst);
-    n = extent(rows, d, ld_);
-    ld = ld_;
-    step = tile_rows * ld_;
-    p = lo + (row * ld_ + c);
+    n = extent(rows, d, ld);
+    p = lo + (row * ld + c);
   }
   // VEC channels of step t of the tile, `left` of them in front of d
-  __device__ __forceinline__ void store(int t, int left, const float *v) const {
+  __device__ __forceinline__ void store(int t, int ld, int left, const float *v) const {
     constexpr int VEC = gated_vec<T>();
-    T *q = p + t * ld;
+    T *q = p + (int64_t)ld * t;
     if constexpr (ASYNC) {
       if (left > 0 && in_bounds(q - lo, n - (VEC - 1), kBndAct)) st_vec<T, VEC>(q, 0, VEC, v);
     } else {
@@ -336,6 +325,7 @@ template <typename T, bool ASYNC> struct GatedDst {
         if (e < left && in_bounds(q + e - lo, n, kBndAct)) st_vec<T, 1>(q, e, VEC, v + e);
     }
   }
+  __device__ __forceinline__ void next(int ld, int tile_rows) { p += (int64_t)ld * tile_rows; }
 };
 
 // ----------------------------------------------------------------- forward
@@ -344,7 +334,7 @@ template <typename T, bool ASYNC> struct GatedDst {
 // w = 1 - a^2), two more with z; the decay's exponential is a polynomial
 // (decay2), which also gives 1 - a without cancellation.
 template <typename T, bool ASYNC, bool GATE, bool START>
-__global__ void __launch_bounds__(kGatedThreads, SSM_GF) gated_fwd_kernel(const GatedParams p) {
+__global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kernel(const GatedParams p) {
   constexpr int STEPS = kGatedFwdSteps, VEC = gated_vec<T>(), E = STEPS * VEC, NT = GATE ? 4 : 3;
   constexpr int kRows = STEPS * kGatedRowBytes;  // bytes of a tensor's rows for a warp
   extern __shared__ __align__(16) char stage[];
@@ -368,13 +358,13 @@ __global__ void __launch_bounds__(kGatedThreads, SSM_GF) gated_fwd_kernel(const 
   const int t_lane = t_warp + part * STEPS;
   const int t_copy = ASYNC ? t_warp + lane % 8 / (8 / S) * STEPS : t_lane;
   GatedSrc<T, ASYNC, STEPS> su, sa, sg, sz;
-  su.init(p.u, p.u_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
-  sa.init(p.ga, p.ga_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
-  sg.init(p.gx, p.gx_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
-  if constexpr (GATE) sz.init(p.z, p.z_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
+  su.init(p.u, p.u_ld, i * p.L + t_warp, c0, lane, R, p.d, S);
+  sa.init(p.ga, p.ga_ld, i * p.L + t_warp, c0, lane, R, p.d, S);
+  sg.init(p.gx, p.gx_ld, i * p.L + t_warp, c0, lane, R, p.d, S);
+  if constexpr (GATE) sz.init(p.z, p.z_ld, i * p.L + t_warp, c0, lane, R, p.d, S);
   const int piece = gated_piece<T, ASYNC>(c0, lane, p.d, S);
   GatedDst<T, ASYNC> dy;
-  dy.init(p.y, p.y_ld, i * p.L + t_lane, tile_rows, c, R, p.d);
+  dy.init(p.y, p.y_ld, i * p.L + t_lane, c, R, p.d);
   const int left = (int)(p.d - c < VEC ? p.d - c : VEC);  // channels in front of d
   float h[VEC];  // state in front of the cluster's next tiles
 #pragma unroll
@@ -393,10 +383,10 @@ __global__ void __launch_bounds__(kGatedThreads, SSM_GF) gated_fwd_kernel(const 
     if (it < iters) {
       const int n = rows_of(t_copy, it);
       char *s = mine + (it & 1) * kHalf;
-      su.fetch(s, n, piece, lane);
-      sa.fetch(s + kRows, n, piece, lane);
-      sg.fetch(s + 2 * kRows, n, piece, lane);
-      if constexpr (GATE) sz.fetch(s + 3 * kRows, n, piece, lane);
+      su.fetch(s, n, piece, lane, p.u_ld, tile_rows);
+      sa.fetch(s + kRows, n, piece, lane, p.ga_ld, tile_rows);
+      sg.fetch(s + 2 * kRows, n, piece, lane, p.gx_ld, tile_rows);
+      if constexpr (GATE) sz.fetch(s + 3 * kRows, n, piece, lane, p.z_ld, tile_rows);
       if (START) {
         const int t = t_warp + it * tile_rows + lane;
         const int64_t r = i * p.L + t;
@@ -521,13 +511,13 @@ __global__ void __launch_bounds__(kGatedThreads, SSM_GF) gated_fwd_kernel(const 
     }
     if (n == STEPS) {
 #pragma unroll
-      for (int t = 0; t < STEPS; ++t) dy.store(t, left, x + t * VEC);
+      for (int t = 0; t < STEPS; ++t) dy.store(t, p.y_ld, left, x + t * VEC);
     } else {
 #pragma unroll
       for (int t = 0; t < STEPS; ++t)
-        if (t < n) dy.store(t, left, x + t * VEC);
+        if (t < n) dy.store(t, p.y_ld, left, x + t * VEC);
     }
-    dy.p += dy.step;
+    dy.next(p.y_ld, tile_rows);
   }
   if (p.h_last && rank == 0 && warp == 0 && part == 0) {
 #pragma unroll
@@ -544,7 +534,7 @@ __global__ void __launch_bounds__(kGatedThreads, SSM_GF) gated_fwd_kernel(const 
 // below), two more with z.  a, f, a^2 / f, g and the adjoint stay in registers; r
 // is put back over the staged gates it came from.
 template <typename T, bool ASYNC, bool GATE, bool START>
-__global__ void __launch_bounds__(kGatedThreads, SSM_GB) gated_bwd_kernel(const GatedBwdParams q_) {
+__global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_bwd_kernel(const GatedBwdParams q_) {
   const GatedParams &p = q_.f;
   constexpr int STEPS = kGatedBwdSteps, VEC = gated_vec<T>(), E = STEPS * VEC, NT = GATE ? 5 : 4;
   constexpr int kRows = STEPS * kGatedRowBytes;  // bytes of a tensor's rows for a warp
@@ -574,17 +564,17 @@ __global__ void __launch_bounds__(kGatedThreads, SSM_GB) gated_bwd_kernel(const 
   const int t_lane = t_warp + part * STEPS;
   const int t_copy = ASYNC ? t_warp + lane % 8 / (8 / S) * STEPS : t_lane;
   GatedSrc<T, ASYNC, STEPS> su, s_a, sg, so, sz;
-  su.init(p.u, p.u_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
-  s_a.init(p.ga, p.ga_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
-  sg.init(p.gx, p.gx_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
-  so.init(q_.dout, q_.dout_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
-  if constexpr (GATE) sz.init(p.z, p.z_ld, i * p.L + t_warp, tile_rows, c0, lane, R, p.d, S);
+  su.init(p.u, p.u_ld, i * p.L + t_warp, c0, lane, R, p.d, S);
+  s_a.init(p.ga, p.ga_ld, i * p.L + t_warp, c0, lane, R, p.d, S);
+  sg.init(p.gx, p.gx_ld, i * p.L + t_warp, c0, lane, R, p.d, S);
+  so.init(q_.dout, q_.dout_ld, i * p.L + t_warp, c0, lane, R, p.d, S);
+  if constexpr (GATE) sz.init(p.z, p.z_ld, i * p.L + t_warp, c0, lane, R, p.d, S);
   const int piece = gated_piece<T, ASYNC>(c0, lane, p.d, S);
   GatedDst<T, ASYNC> du_, da_, dg_, dz_;
-  du_.init(q_.du, q_.du_ld, i * p.L + t_lane, tile_rows, c, R, p.d);
-  da_.init(q_.dga, q_.dga_ld, i * p.L + t_lane, tile_rows, c, R, p.d);
-  dg_.init(q_.dgx, q_.dgx_ld, i * p.L + t_lane, tile_rows, c, R, p.d);
-  if constexpr (GATE) dz_.init(q_.dz, q_.dz_ld, i * p.L + t_lane, tile_rows, c, R, p.d);
+  du_.init(q_.du, q_.du_ld, i * p.L + t_lane, c, R, p.d);
+  da_.init(q_.dga, q_.dga_ld, i * p.L + t_lane, c, R, p.d);
+  dg_.init(q_.dgx, q_.dgx_ld, i * p.L + t_lane, c, R, p.d);
+  if constexpr (GATE) dz_.init(q_.dz, q_.dz_ld, i * p.L + t_lane, c, R, p.d);
   const int left = (int)(p.d - c < VEC ? p.d - c : VEC);  // channels in front of d
   float mu[VEC];                          // adjoint behind the cluster's next tiles
   float2 sA = f2(0.0f), sa = sA, sx = sA;  // sums of dl r, dgate_a / A, dgate_x
@@ -607,11 +597,11 @@ __global__ void __launch_bounds__(kGatedThreads, SSM_GB) gated_bwd_kernel(const 
     if (it < iters) {
       const int n = rows_of(t_copy, it);
       char *s = mine + (it & 1) * kHalf;
-      su.fetch(s, n, piece, lane);
-      s_a.fetch(s + kRows, n, piece, lane);
-      sg.fetch(s + 2 * kRows, n, piece, lane);
-      so.fetch(s + 3 * kRows, n, piece, lane);
-      if constexpr (GATE) sz.fetch(s + 4 * kRows, n, piece, lane);
+      su.fetch(s, n, piece, lane, p.u_ld, tile_rows);
+      s_a.fetch(s + kRows, n, piece, lane, p.ga_ld, tile_rows);
+      sg.fetch(s + 2 * kRows, n, piece, lane, p.gx_ld, tile_rows);
+      so.fetch(s + 3 * kRows, n, piece, lane, q_.dout_ld, tile_rows);
+      if constexpr (GATE) sz.fetch(s + 4 * kRows, n, piece, lane, p.z_ld, tile_rows);
       if (START) {
         const int t = t_warp + it * tile_rows + lane;
         const int64_t r = i * p.L + t;
@@ -817,16 +807,16 @@ __global__ void __launch_bounds__(kGatedThreads, SSM_GB) gated_bwd_kernel(const 
       for (int e = 0; e < 2; e += VEC) {
         const int t = (2 * q + e) / VEC;
         if (t >= n) continue;
-        du_.store(t, left, vu + e);
-        da_.store(t, left, va + e);
-        dg_.store(t, left, vg + e);
-        if constexpr (GATE) dz_.store(t, left, vz + e);
+        du_.store(t, q_.du_ld, left, vu + e);
+        da_.store(t, q_.dga_ld, left, va + e);
+        dg_.store(t, q_.dgx_ld, left, vg + e);
+        if constexpr (GATE) dz_.store(t, q_.dz_ld, left, vz + e);
       }
     }
-    du_.p += du_.step;
-    da_.p += da_.step;
-    dg_.p += dg_.step;
-    if constexpr (GATE) dz_.p += dz_.step;
+    du_.next(q_.du_ld, tile_rows);
+    da_.next(q_.dga_ld, tile_rows);
+    dg_.next(q_.dgx_ld, tile_rows);
+    if constexpr (GATE) dz_.next(q_.dz_ld, tile_rows);
   }
   if (q_.dh0 && rank == 0 && warp == 0 && part == 0) {
 #pragma unroll
