@@ -526,24 +526,36 @@ class _Pool:
         if stream is not None and not hasattr(stream, "cuda_stream"):
             self.stream = torch.cuda.ExternalStream(int(stream), device=device)
 
-    def empty(self, shape, dtype):
+    def like(self, t, dtype=None):
+        """A contiguous tensor of t's shape (and type)."""
         if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
         with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+
+    def new(self, t, shape, dtype):
+        """A tensor of this shape and type on t's device."""
+        if self.stream is None:
+            return t.new_empty(shape, dtype=dtype)
+        with torch.cuda.stream(self.stream):
+            return t.new_empty(shape, dtype=dtype)
 
 
-def _workspace(workspace, nbytes, pool):
+def _workspace(workspace, nbytes, pool, ref):
     """(tensor, pointer, bytes) of the given workspace, or of one from the pool
     for the bytes the library asks for on its device."""
     if workspace is None:
-        with torch.cuda.device(pool.device):
-            workspace = pool.empty(max(int(nbytes()), 1), torch.uint8)
-    else:
-        if not isinstance(workspace, torch.Tensor):
-            raise TypeError("workspace: expected a torch.Tensor")
-        if workspace.device != pool.device or not workspace.is_contiguous():
-            raise ValueError(f"workspace: must be contiguous on {pool.device}")
+        if pool.device.index == torch._C._cuda_getDevice():
+            n = nbytes()
+        else:
+            with torch.cuda.device(pool.device):
+                n = nbytes()
+        workspace = pool.new(ref, max(int(n), 1), torch.uint8)
+        return workspace, workspace.data_ptr(), int(n)
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace: expected a torch.Tensor")
+    if workspace.device != pool.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous on {pool.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -595,23 +607,30 @@ def ssm_gated_scan_fwd(u, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, s
     _need(h_last, "h_last", (b, d), torch.float32, dev)
     states = _chunk_states(chunk_states, "chunk_states", b, L, d, dev)
     if y is None:
-        y = _Pool(dev, stream).empty(shape, u.dtype)
+        y = _Pool(dev, stream).like(u)
     _launch(_lib.ssm_gated_scan_fwd, "ssm_gated_scan_fwd", dev, stream, *ins, _ptr(seq_start),
             _ptr(h0), _ptr(h_last), *_rows(y, "y", shape, u.dtype, dev), *states, b, L, d, code)
     return y
 
 
-def _outputs(out, spec, pool, dev):
-    """The outputs named in spec ({name: (shape, dtype, strided)}), from
-    ``out`` where it has them, else new."""
-    got = {}
-    for name, (shape, dtype, strided) in spec.items():
-        t = None if out is None else out.get(name)
-        if t is None:
-            t = pool.empty(shape, dtype)
-        elif not strided:
-            _need(t, name, shape, dtype, dev)
-        got[name] = t
+def _outputs(out, likes, params, pool, dev):
+    """The outputs {name: tensor}, from ``out`` where it has them, else new: likes
+    {name: a tensor of its shape and type, as contiguous rows}, params {name: the
+    fp32 parameter it is the gradient of}."""
+    if out is None:
+        got = {k: pool.like(t) for k, t in likes.items()}
+        if len(params) > 1 and len({t.shape for t in params.values()}) == 1:
+            ref = next(iter(params.values()))  # one allocation, a row for each
+            got.update(zip(params, pool.new(ref, (len(params), *ref.shape), torch.float32).unbind(0)))
+        else:
+            got.update((k, pool.like(t)) for k, t in params.items())
+        return got
+    got = {k: pool.like(t) if out.get(k) is None else out[k] for k, t in likes.items()}
+    for k, t in params.items():
+        g = out.get(k)
+        if g is not None:
+            _need(g, k, t.shape, torch.float32, dev)
+        got[k] = pool.like(t) if g is None else g
     return got
 
 
@@ -637,16 +656,23 @@ def ssm_gated_scan_bwd(u, gate_a, gate_x, A, dout, states, bias_a=None, bias_x=N
         raise TypeError("states: expected the chunk_states of ssm_gated_scan_fwd")
     states = _chunk_states(states, "states", b, L, d, dev)
     pool = _Pool(dev, stream)
-    rows = ["du", "dgate_a", "dgate_x"] + (["dz"] if z is not None else [])
-    spec = {k: (shape, act, True) for k in rows}
-    spec["dA"] = ((d,), f32, False)
-    spec.update({"d" + k: ((d,), f32, False) for k, on in (("bias_a", bias_a), ("bias_x", bias_x))
-                 if on is not None})
+    if A is None:
+        raise TypeError("A: expected a torch.Tensor")
+    likes = dict(du=u, dgate_a=u, dgate_x=u)
+    if z is not None:
+        likes["dz"] = u
+    params = dict(dA=A)
+    if bias_a is not None:
+        params["dbias_a"] = bias_a
+    if bias_x is not None:
+        params["dbias_x"] = bias_x
+    g = _outputs(out, likes, params, pool, dev)
     if want_dh0:
-        spec["dh0"] = ((b, d), f32, False)
-    g = _outputs(out, spec, pool, dev)
+        dh0 = None if out is None else out.get("dh0")
+        _need(dh0, "dh0", (b, d), f32, dev)
+        g["dh0"] = pool.new(A, (b, d), f32) if dh0 is None else dh0
     ws, ws_ptr, ws_bytes = _workspace(
-        workspace, lambda: _lib.ssm_gated_scan_bwd_workspace_bytes(b, L, d), pool)
+        workspace, lambda: _lib.ssm_gated_scan_bwd_workspace_bytes(b, L, d), pool, A)
     grads = [v for k in ("du", "dgate_a", "dgate_x", "dz")
              for v in _rows(g.get(k), k, shape, act, dev)]
     _launch(_lib.ssm_gated_scan_bwd, "ssm_gated_scan_bwd", dev, stream, *ins, _ptr(seq_start),
@@ -670,7 +696,7 @@ def ssm_gated_state_update(state, u, gate_a, gate_x, A, bias_a=None, bias_x=None
         raise TypeError("state: expected a torch.Tensor")
     _need(state, "state", shape, torch.float32, dev)
     if y is None:
-        y = _Pool(dev, stream).empty(shape, u.dtype)
+        y = _Pool(dev, stream).like(u)
     _launch(_lib.ssm_gated_state_update, "ssm_gated_state_update", dev, stream, _ptr(state), *ins,
             *_rows(y, "y", shape, u.dtype, dev), shape[0], shape[1], code)
     return y
@@ -703,7 +729,7 @@ def ssm_conv1d_fwd(x, weight, bias=None, silu=True, conv_state=None, conv_state_
     _need(conv_state_out, "conv_state_out", (b, d, K), x.dtype, dev)
     _need(seq_start, "seq_start", (b, L), torch.uint8, dev)
     if y is None:
-        y = _Pool(dev, stream).empty(shape, x.dtype)
+        y = _Pool(dev, stream).like(x)
     _launch(_lib.ssm_conv1d_fwd, "ssm_conv1d_fwd", dev, stream, *xr, _ptr(weight), _ptr(bias),
             int(bool(silu)), _ptr(conv_state), _ptr(conv_state_out), _ptr(seq_start),
             *_rows(y, "y", shape, x.dtype, dev), b, L, d, K, code)
@@ -729,12 +755,12 @@ def ssm_conv1d_bwd(x, weight, dy, bias=None, silu=True, conv_state=None, seq_sta
     _need(conv_state, "conv_state", (b, d, K), act, dev)
     _need(seq_start, "seq_start", (b, L), torch.uint8, dev)
     pool = _Pool(dev, stream)
-    spec = dict(dx=(shape, act, True), dweight=((d, K), f32, False))
+    params = dict(dweight=weight)
     if bias is not None:
-        spec["dbias"] = ((d,), f32, False)
-    g = _outputs(out, spec, pool, dev)
+        params["dbias"] = bias
+    g = _outputs(out, dict(dx=x), params, pool, dev)
     ws, ws_ptr, ws_bytes = _workspace(
-        workspace, lambda: _lib.ssm_conv1d_bwd_workspace_bytes(b, L, d, K), pool)
+        workspace, lambda: _lib.ssm_conv1d_bwd_workspace_bytes(b, L, d, K), pool, weight)
     _launch(_lib.ssm_conv1d_bwd, "ssm_conv1d_bwd", dev, stream, *xr, _ptr(weight), _ptr(bias),
             int(bool(silu)), _ptr(conv_state), _ptr(seq_start), *_rows(dy, "dy", shape, act, dev),
             *_rows(g["dx"], "dx", shape, act, dev), _ptr(g["dweight"]), _ptr(g.get("dbias")), b, L, d,
@@ -755,7 +781,7 @@ def ssm_conv1d_update(conv_state, x, weight, bias=None, silu=True, y=None, strea
         raise TypeError("conv_state: expected a torch.Tensor")
     _need(conv_state, "conv_state", (*shape, K), x.dtype, dev)
     if y is None:
-        y = _Pool(dev, stream).empty(shape, x.dtype)
+        y = _Pool(dev, stream).like(x)
     _launch(_lib.ssm_conv1d_update, "ssm_conv1d_update", dev, stream, _ptr(conv_state), *xr,
             _ptr(weight), _ptr(bias), int(bool(silu)), *_rows(y, "y", shape, x.dtype, dev), shape[0],
             shape[1], K, code)
@@ -782,7 +808,7 @@ def ssm_gated_norm_fwd(x, z, weight, groups=1, eps=1e-5, norm_before_gate=False,
     xr, zr = _rows(x, "x", shape, act, dev), _rows(z, "z", shape, act, dev)
     _need(weight, "weight", (d,), torch.float32, dev)
     if y is None:
-        y = _Pool(dev, stream).empty(shape, act)
+        y = _Pool(dev, stream).like(x)
     _launch(_lib.ssm_gated_norm_fwd, "ssm_gated_norm_fwd", dev, stream, *xr, *zr, _ptr(weight), groups,
             eps, int(bool(norm_before_gate)), *_rows(y, "y", shape, act, dev), _row_count(shape), d,
             code)
@@ -808,12 +834,12 @@ def ssm_gated_norm_bwd(x, z, weight, dy, groups=1, eps=1e-5, norm_before_gate=Fa
     _need(weight, "weight", (d,), torch.float32, dev)
     dyr = _rows(dy, "dy", shape, act, dev)
     pool = _Pool(dev, stream)
-    spec = dict(dx=(shape, act, True), dweight=((d,), torch.float32, False))
-    if z is not None:
-        spec["dz"] = (shape, act, True)
-    g = _outputs(out, spec, pool, dev)
+    if weight is None:
+        raise TypeError("weight: expected a torch.Tensor")
+    likes = dict(dx=x) if z is None else dict(dx=x, dz=x)
+    g = _outputs(out, likes, dict(dweight=weight), pool, dev)
     ws, ws_ptr, ws_bytes = _workspace(
-        workspace, lambda: _lib.ssm_gated_norm_bwd_workspace_bytes(rows, d, groups), pool)
+        workspace, lambda: _lib.ssm_gated_norm_bwd_workspace_bytes(rows, d, groups), pool, weight)
     _launch(_lib.ssm_gated_norm_bwd, "ssm_gated_norm_bwd", dev, stream, *xr, *zr, _ptr(weight), groups,
             eps, int(bool(norm_before_gate)), *dyr, *_rows(g["dx"], "dx", shape, act, dev),
             *_rows(g.get("dz"), "dz", shape, act, dev), _ptr(g["dweight"]), rows, d, code, ws_ptr,
@@ -852,9 +878,9 @@ def ssm_add_norm_fwd(x, residual, weight, scale=None, post_weight=None, eps=1e-5
     _need(post_weight, "post_weight", (d,), f32, dev)
     pool = _Pool(dev, stream)
     if y is None:
-        y = pool.empty(shape, act)
+        y = pool.like(x)
     if residual_out is None:
-        residual_out = pool.empty(shape, residual_dtype)
+        residual_out = pool.like(x, residual_dtype)
     _launch(_lib.ssm_add_norm_fwd, "ssm_add_norm_fwd", dev, stream, *xr, *rr, _ptr(weight),
             _ptr(post_weight), _ptr(scale), eps, *_rows(y, "y", shape, act, dev),
             *_rows(residual_out, "residual_out", shape, residual_dtype, dev), _row_count(shape), d,
@@ -895,15 +921,19 @@ def ssm_add_norm_bwd(x, residual_out, weight, dy, dresidual_out=None, scale=None
     dyr = _rows(dy, "dy", shape, act, dev)
     dror = _rows(dresidual_out, "dresidual_out", shape, res, dev)
     pool = _Pool(dev, stream)
-    spec = dict(dx=(shape, act, True), dweight=((d,), f32, False))
+    if weight is None:
+        raise TypeError("weight: expected a torch.Tensor")
+    likes = dict(dx=dy)
     if want_dresidual:
-        spec["dresidual"] = (shape, res, True)
-    for k, on in (("dpost_weight", post_weight), ("dscale", scale)):
-        if on is not None:
-            spec[k] = ((d,), f32, False)
-    g = _outputs(out, spec, pool, dev)
+        likes["dresidual"] = residual_out
+    params = dict(dweight=weight)
+    if post_weight is not None:
+        params["dpost_weight"] = post_weight
+    if scale is not None:
+        params["dscale"] = scale
+    g = _outputs(out, likes, params, pool, dev)
     ws, ws_ptr, ws_bytes = _workspace(
-        workspace, lambda: _lib.ssm_add_norm_bwd_workspace_bytes(rows, d), pool)
+        workspace, lambda: _lib.ssm_add_norm_bwd_workspace_bytes(rows, d), pool, weight)
     _launch(_lib.ssm_add_norm_bwd, "ssm_add_norm_bwd", dev, stream, *xr, *rr, _ptr(weight),
             _ptr(post_weight), _ptr(scale), eps, *dyr, *dror, *_rows(g["dx"], "dx", shape, act, dev),
             *_rows(g.get("dresidual"), "dresidual", shape, res, dev), _ptr(g["dweight"]),
