@@ -469,16 +469,16 @@ ssm_status check_conv(const char *what, Args &a, const ssm::ConvParams &p, int64
 // loads are in flight together (bf16, 16384 x 1536, forward: 3 a thread 31 us, 2
 // 38, 1 49; backward 80, 84, 128).  Where all rows together do not fill the device,
 // the fewest vectors a thread instead (64 rows: 2.6 us against 3.5).  tpr = 0: longer
-// than 512 threads of 4 vectors hold.
+// than 512 threads of `most` vectors hold.
 struct NormPlan {
   int tpr = 0, vpt = 0, threads = 0;
 };
-NormPlan norm_plan(int64_t rows, int64_t nv) {
+NormPlan norm_plan(int64_t rows, int64_t nv, int most = 4) {
   NormPlan best;
   int64_t least = -1;
   const bool few = rows * nv < 512 * (int64_t)device_sms();
   for (int tpr = 8; tpr <= ssm::kNormMaxTpr; tpr *= 2)
-    for (int vpt = 1; vpt <= 4; ++vpt) {
+    for (int vpt = 1; vpt <= most; ++vpt) {
       const int64_t idle = (int64_t)tpr * vpt - nv;
       if (idle < 0) continue;
       const int64_t cost = few ? vpt * (int64_t)65536 + tpr : idle;
@@ -493,16 +493,18 @@ NormPlan norm_plan(int64_t rows, int64_t nv) {
 }
 // CTAs of `threads` threads that an SM holds of a kernel, at most four: the
 // backward runs in one wave of them, each with a partial row of the parameters'
-// gradients (per group).
+// gradients (per group).  Asked for the most shared memory a call of it takes, so
+// that the answer, and with it the order of the sums, is the same for every call.
 constexpr int kNormMaxCtas = 4;
-template <auto Kernel> int norm_ctas(int threads, int smem) {
-  static int cached[64][3] = {};
+constexpr int kNormMostSmem = ssm::kNormThreads * 4 * ssm::kNormBwdElems * 4;
+template <auto Kernel> int norm_ctas(int threads) {
+  static int cached[64][2] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-  int &c = cached[dev][threads <= 256 ? 0 : 1];
+  int &c = cached[dev][threads <= ssm::kNormThreads ? 0 : 1];
   if (!c) {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, threads, (size_t)smem) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, threads, kNormMostSmem) != cudaSuccess) {
       cudaGetLastError();
       n = 1;
     }
@@ -580,7 +582,7 @@ ssm_status gated_norm_bwd_e(ssm::GatedNormBwdParams q, int64_t *parts, cudaStrea
   const int smem = norm_smem(n, p.d / p.groups);
   return by_vpt<4>(n.vpt, [&](auto vpt) {
     constexpr auto kernel = ssm::gated_norm_bwd_kernel<T, E, decltype(vpt)::value, FORM>;
-    *parts = norm_parts(p.rows, p.groups, n, norm_ctas<kernel>(n.threads, smem));
+    *parts = norm_parts(p.rows, p.groups, n, norm_ctas<kernel>(n.threads));
     q.parts = (int)*parts;
     if (*parts > kMaxGrid / p.groups) return fail(SSM_ERR_UNSUPPORTED, "%s: too many groups", what);
     kernel<<<(unsigned)(*parts * p.groups), n.threads, smem, st>>>(q);
@@ -644,7 +646,13 @@ template <typename T, typename R> ssm_status add_norm_fwd_any(const ssm::AddNorm
 template <typename T, typename R, int E, bool POST, bool SCALE>
 ssm_status add_norm_bwd_f(ssm::AddNormBwdParams q, int64_t *parts, cudaStream_t st) {
   const char *what = "ssm_add_norm_bwd";
-  const NormPlan n = norm_plan(q.f.rows, q.f.d / E);
+  // with x and its sums at most two vectors a thread, where that leaves no more
+  // than a quarter of the threads idle, else three: more spill (bf16, 16384 x 768,
+  // scale and post norm: 2 a thread 62 us, 3 73)
+  const int64_t nv = q.f.d / E;
+  NormPlan n = norm_plan(q.f.rows, nv, POST || SCALE ? 2 : 4);
+  if ((POST || SCALE) && (n.tpr == 0 || 3 * (int64_t)n.tpr * n.vpt > 4 * nv))
+    n = norm_plan(q.f.rows, nv, 3);
   if (n.tpr == 0) {
     *parts = norm_bwd_parts(q.f.rows);
     ssm::add_norm_bwd_long_kernel<T, R><<<(unsigned)*parts, ssm::kNormThreads, 0, st>>>(q);
@@ -652,9 +660,9 @@ ssm_status add_norm_bwd_f(ssm::AddNormBwdParams q, int64_t *parts, cudaStream_t 
   }
   q.f.tpr = n.tpr;
   const int smem = norm_smem(n, q.f.d);
-  return by_vpt<4>(n.vpt, [&](auto vpt) {
+  return by_vpt<POST || SCALE ? 3 : 4>(n.vpt, [&](auto vpt) {
     constexpr auto kernel = ssm::add_norm_bwd_kernel<T, R, E, decltype(vpt)::value, POST, SCALE>;
-    *parts = norm_parts(q.f.rows, 1, n, norm_ctas<kernel>(n.threads, smem));
+    *parts = norm_parts(q.f.rows, 1, n, norm_ctas<kernel>(n.threads));
     q.parts = (int)*parts;
     kernel<<<(unsigned)*parts, n.threads, smem, st>>>(q);
     return check_launch(what);

@@ -66,10 +66,12 @@ __device__ __forceinline__ bool starts_at(const uint8_t *start, int64_t r, int64
   return in_bounds(r, n, kBndAct) && start[r] != 0;
 }
 
-// Bits of the steps a sequence starts at among `n` (at most N) from s on: one
-// word's load where the bytes are aligned.
+// Bits of the steps a sequence starts at among `n` (at most N) from row r of the
+// `rows` on: one word's load where the bytes are aligned.
 template <int N>
-__device__ __forceinline__ unsigned start_bits(const uint8_t *s, int n) {
+__device__ __forceinline__ unsigned start_bits(const uint8_t *start, int64_t r, int n, int64_t rows) {
+  const uint8_t *s = start + r;
+  if (n <= 0 || !in_bounds(r, rows - ((n < N ? n : N) - 1), kBndAct)) return 0;
   static_assert(N == 4 || N == 8, "one word of start flags");
   using W = typename std::conditional<N == 8, uint2, unsigned>::type;
   unsigned bits = 0;
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kConvThreads, conv_fwd_occ(K)) conv_fwd_kernel
   }
 
   const T *xp = static_cast<const T *>(p.x) + (row + t0) * p.x_ld + c;
-  const uint8_t *sp = START ? p.start + row + t0 : nullptr;
+  int64_t sr = row + t0;  // row of the next start flags
   W raw[kConvRows];
   unsigned st = 0;  // bit q: a sequence starts at row q
   const auto load = [&](int n) {  // the next rows, of which n are the segment's
@@ -202,8 +204,8 @@ __global__ void __launch_bounds__(kConvThreads, conv_fwd_occ(K)) conv_fwd_kernel
     }
     xp += kConvRows * p.x_ld;
     if (START) {
-      st = start_bits<kConvRows>(sp, n);
-      sp += kConvRows;
+      st = start_bits<kConvRows>(p.start, sr, n, p.b * p.L);
+      sr += kConvRows;
     }
   };
   int64_t yo = (row + t0) * p.y_ld + c;
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(kConvThreads, conv_bwd_occ(K, sizeof(T))) conv
     // let out the last dx
     const T *xp = static_cast<const T *>(p.x) + (row + t0) * p.x_ld + c;
     const T *gp = static_cast<const T *>(q.dy) + (row + t0) * q.dy_ld + c;
-    const uint8_t *sp = START ? p.start + row + t0 : nullptr;
+    int64_t sr = row + t0;  // row of the next start flags
     const int all = (int)(t2 - t0), mine = (int)(t1 - t0);
     W rx[N], rg[N];
     unsigned st = 0;
@@ -335,8 +337,8 @@ __global__ void __launch_bounds__(kConvThreads, conv_bwd_occ(K, sizeof(T))) conv
       xp += N * p.x_ld;
       gp += N * q.dy_ld;
       if (START) {
-        st = start_bits<N>(sp, n);
-        sp += N;
+        st = start_bits<N>(p.start, sr, n, R);
+        sr += N;
       }
     };
     int64_t o = (row + t0 - (K - 1)) * q.dx_ld + c;
