@@ -24,6 +24,8 @@
 // kept (4 bytes every 64 steps and channel).
 #pragma once
 
+#include <type_traits>
+
 #include "block_common.cuh"
 
 namespace ssm {
@@ -439,10 +441,19 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kern
     float P[VEC], Q[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) P[e] = 1.0f, Q[e] = 0.0f;
+    // (only where a sequence starts among the warp's steps do they need its care)
+    if (START && any) {
 #pragma unroll
-    for (int q = 0; q < E; q += 2) {
-      gated_step2<VEC, START>(Q, a + q, x + q);
-      gated_prod2<VEC, START>(P, a + q);
+      for (int q = 0; q < E; q += 2) {
+        gated_step2<VEC, true>(Q, a + q, x + q);
+        gated_prod2<VEC, true>(P, a + q);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < E; q += 2) {
+        gated_step2<VEC, false>(Q, a + q, x + q);
+        gated_prod2<VEC, false>(P, a + q);
+      }
     }
     const int par = it & 1;
     float4 front = make_float4(P[0], P[VEC - 1], Q[0], Q[VEC - 1]), own_warp;
@@ -492,15 +503,22 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kern
     }
     if (S > 1) gated_apply<VEC, START>(hs, front);
     // replay
+    const auto replay = [&](auto care) {
+      constexpr bool CARE = decltype(care)::value;
 #pragma unroll
-    for (int q = 0; q < E; q += VEC) {
-      if constexpr (VEC == 2)
-        gated_step2<VEC, START>(hs, a + q, x + q);
-      else
-        hs[0] = through<START>(a[q], hs[0], x[q]);
+      for (int q = 0; q < E; q += VEC) {
+        if constexpr (VEC == 2)
+          gated_step2<VEC, CARE>(hs, a + q, x + q);
+        else
+          hs[0] = through<CARE>(a[q], hs[0], x[q]);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[q + e] = hs[e];
-    }
+        for (int e = 0; e < VEC; ++e) x[q + e] = hs[e];
+      }
+    };
+    if (START && any)
+      replay(std::true_type());
+    else
+      replay(std::false_type());
     if constexpr (GATE) {
 #pragma unroll
       for (int q = 0; q < E / 2; ++q) {
@@ -681,20 +699,28 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_bwd_kern
     float P[VEC], Q[VEC], M[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) P[e] = 1.0f, Q[e] = 0.0f, M[e] = 0.0f;
+    const auto compose = [&](auto care) {  // care: a sequence starts among the warp's steps
+      constexpr bool CARE = decltype(care)::value;
 #pragma unroll
-    for (int q = 0; q < E / 2; ++q) {
-      const float2 u = staged_pair<T>(s, q, lane);
-      const float2 x = mul2(mul2(make_float2(f[2 * q], f[2 * q + 1]), make_float2(g[2 * q], g[2 * q + 1])), u);
-      const float xv[2] = {x.x, x.y};
-      gated_step2<VEC, START>(Q, a + 2 * q, xv);
-      gated_prod2<VEC, START>(P, a + 2 * q);
-    }
-    // mu_t = a_t (go_t + mu_{t+1}); a step that starts a sequence hands nothing back
+      for (int q = 0; q < E / 2; ++q) {
+        const float2 u = staged_pair<T>(s, q, lane);
+        const float2 x =
+            mul2(mul2(make_float2(f[2 * q], f[2 * q + 1]), make_float2(g[2 * q], g[2 * q + 1])), u);
+        const float xv[2] = {x.x, x.y};
+        gated_step2<VEC, CARE>(Q, a + 2 * q, xv);
+        gated_prod2<VEC, CARE>(P, a + 2 * q);
+      }
+      // mu_t = a_t (go_t + mu_{t+1}); a step that starts a sequence hands nothing back
 #pragma unroll
-    for (int q = E - 1; q >= 0; --q) {
-      const float m = a[q] * (lam[q] + M[q % VEC]);
-      M[q % VEC] = START && a[q] == 0.0f ? 0.0f : m;
-    }
+      for (int q = E - 1; q >= 0; --q) {
+        const float m = a[q] * (lam[q] + M[q % VEC]);
+        M[q % VEC] = CARE && a[q] == 0.0f ? 0.0f : m;
+      }
+    };
+    if (START && any)
+      compose(std::true_type());
+    else
+      compose(std::false_type());
     const int par = it & 1;
     // in the warp: back, what lies behind the lane's steps; ahead, in front of them
     float4 back = make_float4(P[0], P[VEC - 1], M[0], M[VEC - 1]), own_warp;
