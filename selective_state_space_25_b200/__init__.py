@@ -1,6 +1,8 @@
 """B200-native selective scan: Mamba's selective scan, VMamba's SS2D
-four-direction scan and the one-token ``Mamba.step()`` state update, as
-hand-written sm_100a CUDA kernels behind a C ABI (``include/ssmscan.h``).
+four-direction scan and the one-token ``Mamba.step()`` state update, and the
+operators around the scan in a recurrent block (gated linear recurrence, causal
+convolution, gated and residual norms), as hand-written sm_100a CUDA kernels
+behind a C ABI (``include/ssmscan.h``).
 
 ``selective_state_space_25_b200.ssmscan`` is the thin Python binding (ctypes
 over ``libssmscan.so``; argument marshalling only).  It is imported lazily so

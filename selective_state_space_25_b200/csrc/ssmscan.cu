@@ -557,7 +557,7 @@ extern "C" {
 
 const char *ssm_last_error(void) { return g_last_error.c_str(); }
 
-const char *ssm_version(void) { return "0.1.0"; }
+const char *ssm_version(void) { return "0.2.0"; }
 
 size_t ssm_scan_fwd_workspace_bytes(int64_t b, int64_t L, int64_t d_in, int64_t d_state) {
   int64_t t;
