@@ -174,20 +174,25 @@ __device__ __forceinline__ float4 shfl4(float4 v, int lane) {
                      __shfl_sync(~0u, v.z, lane), __shfl_sync(~0u, v.w, lane));
 }
 
-// The parts of a warp in the order they are taken (FIRST: part 0 first, else the
-// last part first): own becomes the composition of the parts in front of this
-// lane's, all that of the warp's.
-template <int VEC, bool START, bool FIRST>
+// The parts of a warp in the order they are taken (FORWARD: part 0 first, else the
+// last part first): own becomes the composition of the parts taken before this
+// lane's (not to be used by the part taken first), all, in the lanes of the part
+// taken last, that of the warp's.
+template <int VEC, bool START, bool FORWARD>
 __device__ __forceinline__ void gated_parts(int S, int lane, float4 &own, float4 &all) {
-  const int lc = 32 / S, part = lane / lc, l = lane % lc;
+  all = own;
+  if (S == 1) return;
   const float4 mine = own;
-  own = all = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-  if (S == 1) {
-    all = mine;
+  if (S == 2) {
+    own = shfl4(mine, lane ^ 16);
+    all = own;
+    gated_compose<VEC, START>(all, mine);
     return;
   }
+  const int lc = 32 / S, part = lane / lc, l = lane % lc;
+  all = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
   for (int k = 0; k < S; ++k) {
-    const int s = FIRST ? k : S - 1 - k;
+    const int s = FORWARD ? k : S - 1 - k;
     const float4 m = shfl4(mine, s * lc + l);
     if (s == part) own = all;
     gated_compose<VEC, START>(all, m);
@@ -458,7 +463,8 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kern
     const int par = it & 1;
     float4 front = make_float4(P[0], P[VEC - 1], Q[0], Q[VEC - 1]), own_warp;
     gated_parts<VEC, START, true>(S, lane, front, own_warp);  // in the warp
-    wsum[par][warp][lane] = own_warp;
+    const int l = lane % lc;
+    if (part == S - 1) wsum[par][warp][l] = own_warp;
     __syncthreads();
     float hs[VEC];  // state in front of the warp's steps
     if (C == 1) {  // the warps' maps in order from the tile's start state
@@ -466,7 +472,7 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kern
       for (int e = 0; e < VEC; ++e) hs[e] = h[e];
 #pragma unroll
       for (int w = 0; w < kGatedWarps; ++w) {
-        gated_apply<VEC, START>(h, wsum[par][w][lane]);
+        gated_apply<VEC, START>(h, wsum[par][w][l]);
         if (w + 1 == warp) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) hs[e] = h[e];
@@ -476,10 +482,10 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kern
       // composition of the warps in front of this one; the last warp's, with its
       // own, is the tile's
       float4 ahead = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-      for (int w = 0; w < warp; ++w) gated_compose<VEC, START>(ahead, wsum[par][w][lane]);
+      for (int w = 0; w < warp; ++w) gated_compose<VEC, START>(ahead, wsum[par][w][l]);
       if (warp == kGatedWarps - 1) {
         float4 all = ahead;
-        gated_compose<VEC, START>(all, own_warp);
+        gated_compose<VEC, START>(all, wsum[par][warp][l]);
         for (int w = 0; w < C; ++w) st_peer(&csum[(par * C + rank) * 32 + lane], w, all);
       }
       gated_arrive(warp == kGatedWarps - 1);
@@ -501,7 +507,7 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kern
       for (int e = 0; e < VEC; ++e)
         if (c + e < p.d && in_bounds(o + e, on, kBndChunk)) p.chunk_h[o + e] = hs[e];
     }
-    if (S > 1) gated_apply<VEC, START>(hs, front);
+    if (part > 0) gated_apply<VEC, START>(hs, front);
     // replay
     const auto replay = [&](auto care) {
       constexpr bool CARE = decltype(care)::value;
@@ -603,6 +609,9 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_bwd_kern
       mu[e] = q_.dh_last[i * p.d + c + e];
   }
   unsigned flag = 0;
+  const int64_t nC = (L + kGatedChunk - 1) / kGatedChunk;
+  const float *chunk = p.chunk_h + ((i * nC + (int64_t)(t_warp / kGatedChunk)) * p.d + c);
+  const int64_t chunk_step = (int64_t)(tile_rows / kGatedChunk) * p.d;
   float hnext[VEC];  // state in front of the warp's next chunk
 #pragma unroll
   for (int e = 0; e < VEC; ++e) hnext[e] = 0.0f;
@@ -627,12 +636,12 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_bwd_kern
       }
       const int t_now = t_warp + it * tile_rows;
       if (t_now >= 0 && t_now < L) {  // state in front of the warp's chunk
-        const int64_t nC = (L + kGatedChunk - 1) / kGatedChunk;
-      const int64_t o = (i * nC + t_now / kGatedChunk) * p.d + c, on = p.b * nC * p.d;
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-          if (c + e < p.d && in_bounds(o + e, on, kBndChunk)) hnext[e] = __ldg(p.chunk_h + o + e);
+          if (e < left && in_bounds(chunk + e - p.chunk_h, p.b * nC * p.d, kBndChunk))
+            hnext[e] = __ldg(chunk + e);
       }
+      chunk += chunk_step;
     }
     cp_async_commit();
   };
@@ -727,24 +736,25 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_bwd_kern
     float4 ahead = make_float4(P[0], P[VEC - 1], Q[0], Q[VEC - 1]), fwd_warp;
     gated_parts<VEC, START, false>(S, lane, back, own_warp);
     gated_parts<VEC, START, true>(S, lane, ahead, fwd_warp);
-    wsum[par][warp][lane] = own_warp;
-    wfwd[par][warp][lane] = make_float2(fwd_warp.z, fwd_warp.w);
+    const int l = lane % lc;
+    if (part == 0) wsum[par][warp][l] = own_warp;
+    if (part == S - 1) wfwd[par][warp][l] = make_float2(fwd_warp.z, fwd_warp.w);
     __syncthreads();
     // from the chunk's start state, through its warps in front of this one
     const int first = warp - warp % (kGatedWarps / S);  // of the chunk
     for (int w = first; w < warp; ++w) {
-      const float4 m = wsum[par][w][lane];
-      const float2 x = wfwd[par][w][lane];
+      const float4 m = wsum[par][w][l];
+      const float2 x = wfwd[par][w][l];
       gated_apply<VEC, START>(hs, make_float4(m.x, m.y, x.x, x.y));
     }
-    if (S > 1) gated_apply<VEC, START>(hs, ahead);
+    if (part > 0) gated_apply<VEC, START>(hs, ahead);
     float mb[VEC];  // adjoint behind the warp's steps
     if (C == 1) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) mb[e] = mu[e];
 #pragma unroll
       for (int w = kGatedWarps - 1; w >= 0; --w) {
-        gated_apply<VEC, START>(mu, wsum[par][w][lane]);
+        gated_apply<VEC, START>(mu, wsum[par][w][l]);
         if (w - 1 == warp) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) mb[e] = mu[e];
@@ -753,10 +763,10 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_bwd_kern
     } else {
       // the warps behind this one; the first warp's, with its own, is the tile's
       float4 behind = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-      for (int w = kGatedWarps - 1; w > warp; --w) gated_compose<VEC, START>(behind, wsum[par][w][lane]);
+      for (int w = kGatedWarps - 1; w > warp; --w) gated_compose<VEC, START>(behind, wsum[par][w][l]);
       if (warp == 0) {
         float4 all = behind;
-        gated_compose<VEC, START>(all, own_warp);
+        gated_compose<VEC, START>(all, wsum[par][warp][l]);
         for (int w = 0; w < C; ++w) st_peer(&csum[(par * C + rank) * 32 + lane], w, all);
       }
       gated_arrive(warp == 0);
@@ -770,7 +780,7 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_bwd_kern
       }
       gated_apply<VEC, START>(mb, behind);
     }
-    if (S > 1) gated_apply<VEC, START>(mb, back);
+    if (part < S - 1) gated_apply<VEC, START>(mb, back);
     // the adjoints, last step first
 #pragma unroll
     for (int q = E - 1; q >= 0; --q) {
