@@ -6,7 +6,7 @@
 
 namespace ssm {
 
-// Steps between the states ssm_gated_scan_fwd keeps for its backward.
+// Steps between the states that ssm_gated_scan_fwd keeps for its backward.
 constexpr int kGatedChunk = 32;
 
 // Largest convolution width.
@@ -82,15 +82,7 @@ template <> struct VecWord<float, 1> { using type = float; };
 template <> struct VecWord<float, 2> { using type = float2; };
 template <> struct VecWord<float, 4> { using type = float4; };
 
-template <typename T, int VEC>
-__device__ __forceinline__ typename VecWord<T, VEC>::type ld_raw(const void *p, int64_t i,
-                                                                 int64_t n) {
-  using W = typename VecWord<T, VEC>::type;
-  if (in_bounds(i, n - (VEC - 1), kBndAct))
-    return *reinterpret_cast<const W *>(static_cast<const T *>(p) + i);
-  return W{};
-}
-// The same through the non-coherent path, for data no one writes meanwhile.
+// A load through the non-coherent path, for data no one writes meanwhile.
 template <typename T, int VEC>
 __device__ __forceinline__ typename VecWord<T, VEC>::type ld_raw_ro(const void *p, int64_t i,
                                                                     int64_t n) {

@@ -181,8 +181,8 @@ int64_t gated_chunks(int64_t L) { return (L + ssm::kGatedChunk - 1) / ssm::kGate
 // SM, 24 with as many as it holds (2 of bf16, 3 of fp32); clusters, whose CTAs wait
 // for each other in every round, take a third more; a CTA of 32 bytes of a row (S =
 // 4) a fifth more than one of 64, one of 128 a tenth less.  bf16, b = 8, L = 2048, d
-// = 1536 (us): S = 2 61, S = 1 70, S = 4 70, S = 1 in clusters of 2 81; b = 1, L =
-// 16384, d = 2560: S = 1 in clusters of 8 and S = 2 alone differ 1.3 times.
+// = 1536, when this was fitted (us): S = 2 61, S = 1 70, S = 4 70, S = 1 in clusters
+// of 2 81; b = 1, L = 16384, d = 64: S = 2 178, S = 4 107, S = 4 in clusters of 8 24.
 struct GatedPlan {
   int parts, ctiles, csize;
 };

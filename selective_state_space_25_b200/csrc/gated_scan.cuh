@@ -6,9 +6,9 @@
 //
 // Split over time.  A step is the map h -> a h + x, and maps compose: steps
 // taken together are h -> P h + Q with P the product of their decays.  A CTA's 8
-// warps walk tiles of 64 S steps: a lane takes VEC channels and 8 steps, 32 / S
-// lanes side by side the CTA's channels, the S parts of a warp and the warps
-// consecutive steps.  A lane forms its decays and drives and their (P, Q) in
+// warps walk tiles of 64 S steps (backward 32 S): a lane takes VEC channels and 8
+// (4) steps, 32 / S lanes side by side the CTA's channels, the S parts of a warp and
+// the warps consecutive steps.  A lane forms its decays and drives and their (P, Q) in
 // registers; the parts of a warp combine by shuffles and the warps through shared
 // memory; each composes what lies in front of it onto the tile's start state and
 // then replays its 8 steps from registers.  So every input is read once and
@@ -20,8 +20,13 @@
 //
 // The adjoint is the same recurrence backwards: mu_t = a_t (dout_t + mu_{t+1}) is
 // what step t hands to step t - 1, so the backward composes (P, mu) of tiles from
-// the end, and recomputes the states from the tile start states that the forward
-// kept (4 bytes every 64 steps and channel).
+// the end, and recomputes the states from those that the forward kept (4 bytes
+// every 32 steps and channel).
+//
+// Measured (B200, b = 8, L = 2048, d = 1536, bf16, us): forward 59, backward 134
+// (floors 31 and 54 at the copy bandwidth); with z 70 and 163; fp32 78 and 201 (61,
+// 108).  Bound by instructions and SFU at 16 warps an SM: 41 and some 100 an
+// element, issue slots 56-63 % full.
 #pragma once
 
 #include <type_traits>
@@ -60,7 +65,7 @@ struct GatedBwdParams {
 constexpr int kGatedWarps = 8;  // of a CTA
 constexpr int kGatedThreads = 32 * kGatedWarps;
 // Steps of a lane in a tile, and CTAs an SM holds (bf16 lanes take two channels:
-// 128 registers).  Measured (B200, b = 8, L = 2048, d = 1536, us): bf16 forward 8
+// 128 registers).  Measured at that step (b = 8, L = 2048, d = 1536, us): bf16 forward 8
 // steps with 2 CTAs 61, with 3 (spills) 64, 4 steps with 2, 3, 4 CTAs 76, 73, 79,
 // 16 steps 60 (86 with z, whose stages leave room for one CTA); backward 4 steps
 // with 2 CTAs 145, with 3 (spills) 179, 8 steps with 2 (spills) 178, with 1 168.
