@@ -251,8 +251,8 @@ ssm_status gated_bwd_t(ssm::GatedBwdParams q, int64_t *parts, cudaStream_t st) {
   const GatedPlan g = gated_plan(q.f.b, q.f.L, q.f.d, sizeof(T));
   q.f.parts = g.parts, q.f.ctiles = g.ctiles, q.f.csize = g.csize;
   *parts = q.f.b * g.csize;
-  const int smem = ssm::gated_smem(GATE ? 5 : 4, ssm::kGatedBwdSteps, g.csize);
-  constexpr int most = ssm::gated_smem(GATE ? 5 : 4, ssm::kGatedBwdSteps, ssm::kGatedMaxCluster);
+  const int smem = ssm::gated_smem(GATE ? 5 : 4, ssm::gated_bwd_steps<T>(), g.csize);
+  constexpr int most = ssm::gated_smem(GATE ? 5 : 4, ssm::gated_bwd_steps<T>(), ssm::kGatedMaxCluster);
   if (q.f.start)
     return launch_gated<ssm::gated_bwd_kernel<T, ASYNC, GATE, true>>(q, q.f.b, g, smem, most, st, "ssm_gated_scan_bwd");
   return launch_gated<ssm::gated_bwd_kernel<T, ASYNC, GATE, false>>(q, q.f.b, g, smem, most, st, "ssm_gated_scan_bwd");

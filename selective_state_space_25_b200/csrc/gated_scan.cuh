@@ -6,8 +6,8 @@
 //
 // Split over time.  A step is the map h -> a h + x, and maps compose: steps
 // taken together are h -> P h + Q with P the product of their decays.  A CTA's 8
-// warps walk tiles of 64 S steps (backward 32 S): a lane takes VEC channels and 8
-// (4) steps, 32 / S lanes side by side the CTA's channels, the S parts of a warp and
+// warps walk tiles of 64 S steps (bf16 backward 32 S): a lane takes VEC channels and
+// 8 (4) steps, 32 / S lanes side by side the CTA's channels, the S parts of a warp and
 // the warps consecutive steps.  A lane forms its decays and drives and their (P, Q) in
 // registers; the parts of a warp combine by shuffles and the warps through shared
 // memory; each composes what lies in front of it onto the tile's start state and
@@ -24,9 +24,9 @@
 // every 32 steps and channel).
 //
 // Measured (B200, b = 8, L = 2048, d = 1536, bf16, us): forward 59, backward 134
-// (floors 31 and 54 at the copy bandwidth); with z 70 and 163; fp32 78 and 201 (61,
-// 108).  Bound by instructions and SFU at 16 warps an SM: 41 and some 100 an
-// element, issue slots 56-63 % full.
+// (floors 31 and 54 at the copy bandwidth); with z 70 and 163; fp32 78 and 145 (61,
+// 108).  bf16 is bound by instructions and SFU at 16 warps an SM: 39 and 100
+// an element, issue slots 55-61 % full.
 #pragma once
 
 #include <type_traits>
@@ -69,11 +69,12 @@ constexpr int kGatedThreads = 32 * kGatedWarps;
 // steps with 2 CTAs 61, with 3 (spills) 64, 4 steps with 2, 3, 4 CTAs 76, 73, 79,
 // 16 steps 60 (86 with z, whose stages leave room for one CTA); backward 4 steps
 // with 2 CTAs 145, with 3 (spills) 179, 8 steps with 2 (spills) 178, with 1 168.
-// fp32 forward with 2, 3 CTAs 86, 78, backward 193, 189.
-constexpr int kGatedFwdSteps = 8, kGatedBwdSteps = 4;
+// fp32 forward with 2, 3 CTAs 86, 78; backward 4 steps with 3 CTAs 201, 8 with 2 145.
+constexpr int kGatedFwdSteps = 8;
+template <typename T> constexpr int gated_bwd_steps() { return sizeof(T) == 2 ? 4 : 8; }
 template <typename T> constexpr int gated_ctas() { return sizeof(T) == 2 ? 2 : 3; }
-static_assert(kGatedWarps * kGatedBwdSteps == kGatedChunk && 4 * kGatedFwdSteps <= kGatedChunk,
-              "a backward tile is S chunks, a forward warp starts at most one");
+constexpr int kGatedBwdCtas = 2;
+static_assert(kGatedChunk % (4 * kGatedFwdSteps) == 0, "a chunk is whole warps, whatever S");
 constexpr int kGatedMaxCluster = 8;
 constexpr int kGatedRowBytes = 128;
 
@@ -563,9 +564,9 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kern
 // below), two more with z.  a, f, a^2 / f, g and the adjoint stay in registers; r
 // is put back over the staged gates it came from.
 template <typename T, bool ASYNC, bool GATE, bool START>
-__global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_bwd_kernel(const GatedBwdParams q_) {
+__global__ void __launch_bounds__(kGatedThreads, kGatedBwdCtas) gated_bwd_kernel(const GatedBwdParams q_) {
   const GatedParams &p = q_.f;
-  constexpr int STEPS = kGatedBwdSteps, VEC = gated_vec<T>(), E = STEPS * VEC, NT = GATE ? 5 : 4;
+  constexpr int STEPS = gated_bwd_steps<T>(), VEC = gated_vec<T>(), E = STEPS * VEC, NT = GATE ? 5 : 4;
   constexpr int kRows = STEPS * kGatedRowBytes;  // bytes of a tensor's rows for a warp
   extern __shared__ __align__(16) char stage[];
   __shared__ float4 wsum[2][kGatedWarps][32];       // (P, mu) of the warps' steps
@@ -746,7 +747,7 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_bwd_kern
     if (part == S - 1) wfwd[par][warp][l] = make_float2(fwd_warp.z, fwd_warp.w);
     __syncthreads();
     // from the chunk's start state, through its warps in front of this one
-    const int first = warp - warp % (kGatedWarps / S);  // of the chunk
+    const int first = warp - warp % (kGatedChunk / STEPS / S);  // of the chunk
     for (int w = first; w < warp; ++w) {
       const float4 m = wsum[par][w][l];
       const float2 x = wfwd[par][w][l];
