@@ -84,9 +84,9 @@ typedef enum {
     SSM_ERR_UNSUPPORTED = 2,    /* valid but not compiled: d_state not in {1,2,4,...,64}, unknown dtype */
     SSM_ERR_WORKSPACE = 3,      /* workspace smaller than ssm_scan_fwd_workspace_bytes() */
     SSM_ERR_CUDA = 4,           /* a CUDA runtime call or launch failed (message has the CUDA error) */
-    SSM_ERR_DEVICE_TIMEOUT = 5, /* reserved for a kernel's bounded wait running out; no kernel of
-                                   this build waits on another thread block or device, so no call
-                                   returns it */
+    SSM_ERR_DEVICE_TIMEOUT = 5, /* reserved for a kernel's bounded wait running out; no kernel spins
+                                   on another thread block or device (CTAs of a cluster meet at the
+                                   hardware's cluster barrier), so no call returns it */
     SSM_ERR_DEVICE_BOUNDS = 6   /* debug-bounds build only: a kernel computed a global index outside
                                    its buffer and skipped that access (ssm_check_device_errors) */
 } ssm_status;
