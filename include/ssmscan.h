@@ -513,6 +513,8 @@ ssm_status ss2d_cross_merge(const void *ys, void *y, int64_t b, int64_t H,
  *     y[i,t,d] = z ? h * silu(z[i,t,d]) : h
  * and h_last[i,d] = h after the last step.  A holds log decays, values <= 0
  * (above 0 the root has no value: NaN).
+ * A decay is positive however small (below 2^-126 it is taken as that): a NaN
+ * or an infinite state stays one until a sequence starts.
  *
  *   u, gate_a, gate_x, z, y   device rows (b L, d_in), dtype; z nullable
  *   A                         device fp32 (d_in)

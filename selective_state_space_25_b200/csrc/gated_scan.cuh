@@ -123,13 +123,18 @@ __device__ __forceinline__ float2 silu_2(float2 z) {
 
 // Composition: state after the map (P, Q) from state h.  With START a P of 0
 // says that a sequence started on the way: nothing of h remains, NaN neither.
+// Only a start makes P 0: a step's decay is at least 2^-126 (decay2), and a product
+// of decays is held at the smallest fp32 number, where it would round to 0.  So a
+// NaN or an infinite state stays one until a sequence starts (fma(0, inf, Q) would
+// be NaN, too), and a finite one is off by 2^-149 of itself at most.
+constexpr float kDecayMinP = 1.40129846e-45f;  // 2^-149
 template <bool START> __device__ __forceinline__ float through(float P, float h, float Q) {
   const float r = fmaf(P, h, Q);
   return START && P == 0.0f ? Q : r;
 }
-// Product of two decays; with START one of 0 stays 0 beside a NaN.
+// Product of two maps' decays; with START one of 0 stays 0 beside a NaN.
 template <bool START> __device__ __forceinline__ float times(float P, float a) {
-  const float r = P * a;
+  const float r = max_nan(P * a, kDecayMinP);
   return START && (P == 0.0f || a == 0.0f) ? 0.0f : r;
 }
 
@@ -144,7 +149,7 @@ template <int VEC, bool START> __device__ __forceinline__ void gated_apply(float
   }
 }
 // Flat elements 2 q and 2 q + 1 of a lane (one step of two channels, or two steps
-// of one) taken into the state h and the product P of the decays.
+// of one) taken into the state h, and into the product P of the decays.
 template <int VEC, bool START>
 __device__ __forceinline__ void gated_step2(float (&h)[VEC], const float *a, const float *x) {
   if constexpr (VEC == 2) {
@@ -154,14 +159,18 @@ __device__ __forceinline__ void gated_step2(float (&h)[VEC], const float *a, con
     h[0] = through<START>(a[1], h[0], x[1]);
   }
 }
-template <int VEC, bool START> __device__ __forceinline__ void gated_prod2(float (&P)[VEC], const float *a) {
-  if constexpr (VEC == 2 && !START) {
+template <int VEC> __device__ __forceinline__ void gated_prod2(float (&P)[VEC], const float *a) {
+  if constexpr (VEC == 2) {
     const float2 r = __fmul2_rn(make_float2(P[0], P[1]), make_float2(a[0], a[1]));
     P[0] = r.x, P[1] = r.y;
   } else {
-    P[0] = times<START>(P[0], a[0]);
-    P[VEC - 1] = times<START>(P[VEC - 1], a[1]);
+    P[0] = P[0] * a[0] * a[1];
   }
+}
+// The product of a lane's steps as a map's: 0 where a sequence starts among them.
+template <int VEC> __device__ __forceinline__ void gated_prod_end(float (&P)[VEC], bool start) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) P[e] = start ? 0.0f : max_nan(P[e], kDecayMinP);
 }
 
 // m after `front`, both (P, P, Q, Q) of a lane's channels.
@@ -457,15 +466,16 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kern
 #pragma unroll
       for (int q = 0; q < E; q += 2) {
         gated_step2<VEC, true>(Q, a + q, x + q);
-        gated_prod2<VEC, true>(P, a + q);
+        gated_prod2<VEC>(P, a + q);
       }
     } else {
 #pragma unroll
       for (int q = 0; q < E; q += 2) {
         gated_step2<VEC, false>(Q, a + q, x + q);
-        gated_prod2<VEC, false>(P, a + q);
+        gated_prod2<VEC>(P, a + q);
       }
     }
+    gated_prod_end<VEC>(P, START && bits != 0);
     const int par = it & 1;
     float4 front = make_float4(P[0], P[VEC - 1], Q[0], Q[VEC - 1]), own_warp;
     gated_parts<VEC, START, true>(S, lane, front, own_warp);  // in the warp
@@ -723,8 +733,9 @@ __global__ void __launch_bounds__(kGatedThreads, kGatedBwdCtas) gated_bwd_kernel
             mul2(mul2(make_float2(f[2 * q], f[2 * q + 1]), make_float2(g[2 * q], g[2 * q + 1])), u);
         const float xv[2] = {x.x, x.y};
         gated_step2<VEC, CARE>(Q, a + 2 * q, xv);
-        gated_prod2<VEC, CARE>(P, a + 2 * q);
+        gated_prod2<VEC>(P, a + 2 * q);
       }
+      gated_prod_end<VEC>(P, CARE && bits != 0);
       // mu_t = a_t (go_t + mu_{t+1}); a step that starts a sequence hands nothing back
 #pragma unroll
       for (int q = E - 1; q >= 0; --q) {
