@@ -582,10 +582,13 @@ __global__ void __launch_bounds__(kNormMaxTpr) add_norm_bwd_kernel(const AddNorm
     // the next row's loads in front of the sums (bf16, 32768 x 2048: 120 us, 163 with
     // products by the inverse, whose loads sink to their use); with x the products
     // are faster (16384 x 768, scale and post norm: 61 us, 66).
-    const float rs = rsqrtf(X ? fmaf(s[0], inv, p.eps) : s[0] / (float)p.d + p.eps);
+    // A place without a row holds zeros, which add nothing to the columns' sums while
+    // its inverse roots are finite: not those of eps = 0.
+    const float eps = on ? p.eps : 1.0f;
+    const float rs = rsqrtf(X ? fmaf(s[0], inv, eps) : s[0] / (float)p.d + eps);
     const float mean = X ? s[1] * inv : s[1] / (float)p.d;
     const F k = bc<F>(-mean * rs * rs * rs), rsv = bc<F>(rs);
-    const float rx = POST ? rsqrtf(fmaf(s[2], inv, p.eps)) : 1.0f;
+    const float rx = POST ? rsqrtf(fmaf(s[2], inv, eps)) : 1.0f;
     F sp = bc<F>(0.0f), dv[VPT][N];
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
