@@ -330,8 +330,8 @@ ssm_status check_states(const char *what, const void *p, size_t have, int64_t b,
 // Backward the CTAs of one wave loop over the segments instead, since each
 // writes a partial row of the parameters' gradients.
 struct ConvPlan {
-  int lanes, ctiles, T;
-  int64_t segs, blocks;  // CTAs along the segments
+  int lanes, T;
+  int64_t ctiles, segs, blocks;  // blocks: CTAs along the segments
 };
 ConvPlan conv_plan(int64_t b, int64_t L, int64_t d, int vec, int occ, bool one_wave) {
   ConvPlan best{};
@@ -340,7 +340,7 @@ ConvPlan conv_plan(int64_t b, int64_t L, int64_t d, int vec, int occ, bool one_w
   const int64_t G = d > 0 ? (d + vec - 1) / vec : 1;
   c.lanes = 1;
   while (c.lanes < 32 && c.lanes < G) c.lanes *= 2;
-  c.ctiles = (int)((G + c.lanes - 1) / c.lanes);
+  c.ctiles = (G + c.lanes - 1) / c.lanes;
   const int64_t slots = ssm::kConvThreads / c.lanes;
   const int64_t room = occ * (int64_t)device_sms();
   const int64_t parts = room / c.ctiles > 0 ? room / c.ctiles : 1;
@@ -373,9 +373,9 @@ int64_t conv_bwd_parts(int64_t b, int64_t L, int64_t d) {  // of whichever kerne
 template <typename T, int K, int VEC>
 ssm_status launch_conv_fwd(ssm::ConvParams p, cudaStream_t st) {
   const ConvPlan c = conv_plan(p.b, p.L, p.d, VEC, ssm::conv_fwd_occ(K), false);
-  p.lanes = c.lanes, p.ctiles = c.ctiles, p.T = c.T, p.segs = c.segs;
   if (c.blocks > kMaxGrid / c.ctiles)
     return fail(SSM_ERR_UNSUPPORTED, "ssm_conv1d_fwd: b * L * d_in too large for one grid");
+  p.lanes = c.lanes, p.ctiles = (int)c.ctiles, p.T = c.T, p.segs = c.segs;
   const unsigned grid = (unsigned)(c.blocks * c.ctiles);
   if (p.start)
     ssm::conv_fwd_kernel<T, K, VEC, true><<<grid, ssm::kConvThreads, 0, st>>>(p);
@@ -387,7 +387,9 @@ ssm_status launch_conv_fwd(ssm::ConvParams p, cudaStream_t st) {
 template <typename T, int K, int VEC>
 ssm_status launch_conv_bwd(ssm::ConvBwdParams q, int64_t *parts, cudaStream_t st) {
   const ConvPlan c = conv_plan(q.f.b, q.f.L, q.f.d, VEC, ssm::conv_bwd_occ(K, sizeof(T)), true);
-  q.f.lanes = c.lanes, q.f.ctiles = c.ctiles, q.f.T = c.T, q.f.segs = c.segs;
+  if (c.blocks > kMaxGrid / c.ctiles)
+    return fail(SSM_ERR_UNSUPPORTED, "ssm_conv1d_bwd: b * L * d_in too large for one grid");
+  q.f.lanes = c.lanes, q.f.ctiles = (int)c.ctiles, q.f.T = c.T, q.f.segs = c.segs;
   q.parts = (int)c.blocks;
   *parts = c.blocks;
   const unsigned grid = (unsigned)(c.blocks * c.ctiles);
