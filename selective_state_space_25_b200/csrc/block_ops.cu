@@ -870,6 +870,9 @@ ssm_status ssm_conv1d_fwd(const void *x, int64_t x_ld, const float *weight, cons
   Args a(what, esize(dtype));
   if (ssm_status s = check_conv(what, a, p, d_conv, dtype)) return s;
   if (b * L > 0 && d_in > 0 && !y) return fail(SSM_ERR_INVALID_ARG, "%s: y is required", what);
+  // the kernel that writes the window takes its taps first, of an empty sequence too
+  if (b > 0 && d_in > 0 && conv_state_out && !weight)
+    return fail(SSM_ERR_INVALID_ARG, "%s: weight is required", what);
   const size_t es = esize(dtype);
   a.flat(false, "conv_state", conv_state, b * d_in * d_conv * (int64_t)es, es);
   a.flat(true, "conv_state_out", conv_state_out, b * d_in * d_conv * (int64_t)es, es);

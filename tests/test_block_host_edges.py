@@ -4,6 +4,9 @@ import os
 import subprocess
 import sys
 
+import test_block_host as H
+from selective_state_space_25_b200 import ssmscan as S
+
 # sizes far beyond any memory; the library only counts
 WIDE = """
 from selective_state_space_25_b200 import ssmscan as S
@@ -33,3 +36,10 @@ def test_sizes_beyond_any_memory_are_counted_or_refused():
     r = subprocess.run([sys.executable, "-c", WIDE], capture_output=True, text=True, timeout=120,
                        env=dict(os.environ, PYTHONPATH=":".join(sys.path)))
     assert r.returncode == 0 and "counted" in r.stdout, (r.returncode, r.stderr[-2000:])
+
+
+def test_conv1d_of_an_empty_sequence_needs_its_weight():
+    """With a window to write there is a launch, which takes the weight."""
+    assert H.conv_fwd(L=0, w=None, x=None, y=None) == H.INV and "weight" in S.last_error()
+    assert H.conv_fwd(L=0, w=None, x=None, y=None, cso=None) == H.OK
+    assert H.conv_fwd(L=0, b=0, w=None, x=None, y=None) == H.OK
