@@ -39,6 +39,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
 _SZ = ctypes.c_size_t
+_NO_SIZE = _SZ(-1).value  # a size query's answer for invalid sizes
 
 _lib.ssm_last_error.restype = ctypes.c_char_p
 _lib.ssm_version.restype = ctypes.c_char_p
@@ -543,13 +544,16 @@ class _Pool:
 
 def _workspace(workspace, nbytes, pool, ref):
     """(tensor, pointer, bytes) of the given workspace, or of one from the pool
-    for the bytes the library asks for on its device."""
+    for the bytes the library asks for on its device; none for sizes that it
+    refuses, which the call itself then says."""
     if workspace is None:
         if pool.device.index == torch._C._cuda_getDevice():
             n = nbytes()
         else:
             with torch.cuda.device(pool.device):
                 n = nbytes()
+        if n == _NO_SIZE:
+            return None, None, 0
         workspace = pool.new(ref, max(int(n), 1), torch.uint8)
         return workspace, workspace.data_ptr(), int(n)
     if not isinstance(workspace, torch.Tensor):

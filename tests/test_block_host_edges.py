@@ -4,12 +4,16 @@ import os
 import subprocess
 import sys
 
+import torch
+
 import test_block_host as H
 from selective_state_space_25_b200 import ssmscan as S
 
 # sizes far beyond any memory; the library only counts
 WIDE = """
 from selective_state_space_25_b200 import ssmscan as S
+import torch
+
 import test_block_host as H
 L = S.lib()
 for d in [2 ** k + e for k in range(30, 57) for e in (-1, 0, 1)]:
@@ -43,3 +47,19 @@ def test_conv1d_of_an_empty_sequence_needs_its_weight():
     assert H.conv_fwd(L=0, w=None, x=None, y=None) == H.INV and "weight" in S.last_error()
     assert H.conv_fwd(L=0, w=None, x=None, y=None, cso=None) == H.OK
     assert H.conv_fwd(L=0, b=0, w=None, x=None, y=None) == H.OK
+
+
+def test_binding_leaves_sizes_without_a_workspace_to_the_call(monkeypatch):
+    """(size_t)-1, the library's answer for sizes that it refuses, is no number of
+    bytes to allocate: the call goes on without a workspace, to the refusal."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+
+    class Pool:
+        device = torch.device("cuda", 0)
+
+        def new(self, ref, shape, dtype):
+            return torch.empty(shape, dtype=dtype)
+
+    assert S._workspace(None, lambda: H.NONE, Pool(), None)[1:] == (None, 0)
+    ws, ptr, n = S._workspace(None, lambda: 96, Pool(), None)
+    assert ws.numel() == n == 96 and ptr == ws.data_ptr()
