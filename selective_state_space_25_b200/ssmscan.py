@@ -307,7 +307,7 @@ def ssm_scan_bwd(u, delta, A, B, C, dout, D=None, z=None, dt_bias=None, delta_so
                  dh0=torch.empty((b, d_in, N), dtype=f32, device=dev) if want_dh0 else None)
     if states is not None:
         aux = ssm_scan_bwd_saved_workspace_bytes(b, L, d_in, N)
-        if workspace is None and aux > 0:
+        if workspace is None and 0 < aux < _NO_SIZE:  # else the call says what it refuses
             workspace = torch.empty(aux, dtype=torch.uint8, device=dev)
         st = _lib.ssm_scan_bwd_saved_ex(
             _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
@@ -320,9 +320,9 @@ def ssm_scan_bwd(u, delta, A, B, C, dout, D=None, z=None, dt_bias=None, delta_so
         _check(st, "ssm_scan_bwd_saved")
         return {k: v for k, v in g.items() if v is not None}
     need = ssm_scan_bwd_fast_workspace_bytes(b, L, d_in, N)  # the fastest path's
-    if workspace is None:
+    if workspace is None and need < _NO_SIZE:  # else the call says what it refuses
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _lib.ssm_scan_bwd(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
                            _ptr(dt_bias), int(bool(delta_softplus)), _ptr(h0), _ptr(dout),
                            _ptr(dh_last), _ptr(g["du"]), _ptr(g["ddelta"]), _ptr(g["dA"]),
