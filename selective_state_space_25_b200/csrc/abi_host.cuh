@@ -2,6 +2,7 @@
 // message, argument checks, launches.
 #pragma once
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -107,19 +108,40 @@ ssm_status launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 threads, i
   return ok();
 }
 
+// A number above 0 for each device, found on its first use.  Any thread may ask at
+// any time; two that find it at once find the same.
+class PerDevice {
+ public:
+  // find(device) for the current device; `none` where there is none
+  template <typename F> int get(F &&find, int none) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) {
+      cudaGetLastError();
+      return none;
+    }
+    int v = v_[dev].load(std::memory_order_relaxed);
+    if (!v) v_[dev].store(v = find(dev), std::memory_order_relaxed);
+    return v;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<int> v_[kDevices] = {};
+};
+
 // Opt a kernel into > 48 KB of dynamic shared memory once per device.
 template <auto Kernel>
 ssm_status ensure_smem(int bytes, const char *what) {
-  static bool done[64] = {};
+  static std::atomic<bool> done[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
     return fail(SSM_ERR_CUDA, "%s: cudaGetDevice failed", what);
-  if (!done[dev]) {
+  if (!done[dev].load(std::memory_order_acquire)) {
     const cudaError_t e =
         cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess)
       return fail(SSM_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", what, cudaGetErrorString(e));
-    done[dev] = true;
+    done[dev].store(true, std::memory_order_release);
   }
   return ok();
 }
@@ -127,21 +149,17 @@ ssm_status ensure_smem(int bytes, const char *what) {
 // SMs of the current device (148 on B200; also the answer when no device is
 // visible, so the workspace query works on a host without a GPU).
 inline int device_sms() {
-  static int cached[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-    cudaGetLastError();
-    return 148;
-  }
-  if (!cached[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-      cudaGetLastError();
-      n = 148;
-    }
-    cached[dev] = n;
-  }
-  return cached[dev];
+  static PerDevice sms;
+  return sms.get(
+      [](int dev) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+          cudaGetLastError();
+          n = 148;
+        }
+        return n;
+      },
+      148);
 }
 
 inline unsigned grid_for(int64_t n) {

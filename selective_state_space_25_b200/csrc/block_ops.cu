@@ -500,19 +500,17 @@ NormPlan norm_plan(int64_t rows, int64_t nv, int most = 4) {
 constexpr int kNormMaxCtas = 4;
 constexpr int kNormMostSmem = ssm::kNormThreads * 4 * ssm::kNormBwdElems * 4;
 template <auto Kernel> int norm_ctas(int threads) {
-  static int cached[64][2] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-  int &c = cached[dev][threads <= ssm::kNormThreads ? 0 : 1];
-  if (!c) {
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, threads, kNormMostSmem) != cudaSuccess) {
-      cudaGetLastError();
-      n = 1;
-    }
-    c = n < 1 ? 1 : n > kNormMaxCtas ? kNormMaxCtas : n;
-  }
-  return c;
+  static PerDevice ctas[2];
+  return ctas[threads <= ssm::kNormThreads ? 0 : 1].get(
+      [threads](int) {
+        int n = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, threads, kNormMostSmem) != cudaSuccess) {
+          cudaGetLastError();
+          n = 1;
+        }
+        return n < 1 ? 1 : n > kNormMaxCtas ? kNormMaxCtas : n;
+      },
+      1);
 }
 int64_t norm_parts(int64_t rows, int64_t groups, const NormPlan &n, int ctas) {
   const int64_t slots = n.threads / n.tpr;
