@@ -545,7 +545,8 @@ size_t ssm_gated_scan_states_bytes(int64_t b, int64_t L, int64_t d_in);
  *     dl = lam (a h_{t-1} - a^2 g u / f)   (0 where a sequence starts, and its
  *                                           second term 0 where f = 0)
  *     dA = sum dl r;  dgate_a = dl A r (1 - r);  dh0 = a_0 lam_0
- * dbias_a, dbias_x are the sums of dgate_a, dgate_x over b and L.
+ * dbias_a, dbias_x are the sums of dgate_a, dgate_x over b and L.  Gates below
+ * 2^-60 are taken as that.
  *
  *   dout                       device rows (b L, d_in), dtype
  *   dh_last                    device fp32 (b, d_in), nullable (0)

@@ -176,8 +176,9 @@ bool vec_rows(int64_t vec, size_t es, int64_t d, std::initializer_list<std::pair
 int64_t gated_chunks(int64_t L) { return (L + ssm::kGatedChunk - 1) / ssm::kGatedChunk; }
 
 // Parts of a warp (S) and CTAs of a cluster (C).  A CTA's round is 64 S steps of
-// 1 / S of the channels, the same work whatever S.  In tenths of a microsecond, as
-// measured (forward; the backward goes alike): a round takes 14 with one CTA on an
+// 1 / S of the channels, the same work whatever S (the bf16 backward's is 32 S steps).
+// The rule is the forward's, and the backward, which holds 2 CTAs an SM of either
+// type, takes the same plan.  In tenths of a microsecond, as measured: a round takes 14 with one CTA on an
 // SM, 24 with as many as it holds (2 of bf16, 3 of fp32); clusters, whose CTAs wait
 // for each other in every round, take a third more; a CTA of 32 bytes of a row (S =
 // 4) a fifth more than one of 64, one of 128 a tenth less.  bf16, b = 8, L = 2048, d
@@ -468,9 +469,9 @@ ssm_status check_conv(const char *what, Args &a, const ssm::ConvParams &p, int64
 // -------------------------------------------------------------------- norms
 // Threads of a row of nv vectors and vectors of a thread (1 .. 4): the pair with
 // the fewest idle places, of those the one with the most vectors a thread, whose
-// loads are in flight together (bf16, 16384 x 1536, forward: 3 a thread 31 us, 2
-// 38, 1 49; backward 80, 84, 128).  Where all rows together do not fill the device,
-// the fewest vectors a thread instead (64 rows: 2.6 us against 3.5).  tpr = 0: longer
+// loads are in flight together (bf16, 16384 x 1536, forward: 3 a thread 33 us, 2
+// 35, 1 47; backward 60, 70, 105).  Where all rows together do not fill the device,
+// the fewest vectors a thread instead (64 rows: 2.5 us against 3.2).  tpr = 0: longer
 // than 512 threads of `most` vectors hold.
 struct NormPlan {
   int tpr = 0, vpt = 0, threads = 0;

@@ -1,7 +1,8 @@
-"""Fits the two polynomials the kernels evaluate on the FMA pipe.
+"""Fits the polynomials the kernels evaluate on the FMA pipe.
 
 1. exp2.  2^x = 2^j * p(r) with j = rint(x), r = x - j in [-1/2, 1/2] and
-       p(r) = 1 + r * q(r),   q(r) ~ (2^r - 1) / r,   q of degree 4.
+       p(r) = 1 + r * q(r),   q(r) ~ (2^r - 1) / r,   q of degree 4
+   (degree 5 for the gated recurrence's decay, which needs 1 - 2^x as well).
    Writing p this way makes p(0) = 1 exactly and keeps the RELATIVE accuracy
    of p(r) - 1 = 2^r - 1 near r = 0, which is what a decay factor close to
    one needs (the state's memory is 1 / (1 - 2^x)).
@@ -78,5 +79,7 @@ if __name__ == "__main__":
         print(f"constexpr float kExp2Q{i} = {float(v):.9e}f;")
     for i, v in enumerate(s):
         print(f"constexpr float kLog1pS{i} = {float(v):.9e}f;")
+    for i, v in enumerate(fit_exp2(5)):
+        print(f"constexpr float kDecayQ{i} = {float(v):.9e}f;")
     for k, v in errs.items():
         print(f"// {k}: {v:.3e}")

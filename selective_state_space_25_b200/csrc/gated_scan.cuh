@@ -23,10 +23,11 @@
 // the end, and recomputes the states from those that the forward kept (4 bytes
 // every 32 steps and channel).
 //
-// Measured (B200, b = 8, L = 2048, d = 1536, bf16, us): forward 59, backward 134
-// (floors 31 and 54 at the copy bandwidth); with z 70 and 163; fp32 78 and 145 (61,
-// 108).  bf16 is bound by instructions and SFU at 16 warps an SM: 39 and 100
-// an element, issue slots 55-61 % full.
+// Measured (B200, b = 8, L = 2048, d = 1536, bf16, us): forward 58, backward 135
+// (floors 31 and 54 at the copy bandwidth); with z 70 and 165; fp32 79 and 147 (61,
+// 108).  bf16 is bound by latency at 16 warps an SM and its part-filled second wave
+// (384 CTAs over 296 places): 39 and 100 instructions an element, issue slots 56-62 %
+// full, SFU 47 and 22 %.
 #pragma once
 
 #include <type_traits>
@@ -65,7 +66,7 @@ struct GatedBwdParams {
 constexpr int kGatedWarps = 8;  // of a CTA
 constexpr int kGatedThreads = 32 * kGatedWarps;
 // Steps of a lane in a tile, and CTAs an SM holds (bf16 lanes take two channels:
-// 128 registers).  Measured at that step (b = 8, L = 2048, d = 1536, us): bf16 forward 8
+// 128 registers, of which the backward spills 4 to 44 bytes in most forms).  Measured at that step (b = 8, L = 2048, d = 1536, us): bf16 forward 8
 // steps with 2 CTAs 61, with 3 (spills) 64, 4 steps with 2, 3, 4 CTAs 76, 73, 79,
 // 16 steps 60 (86 with z, whose stages leave room for one CTA); backward 4 steps
 // with 2 CTAs 145, with 3 (spills) 179, 8 steps with 2 (spills) 178, with 1 168.
@@ -354,7 +355,8 @@ template <typename T, bool ASYNC> struct GatedDst {
 // Grid: csize * ctiles * b CTAs in clusters of csize.  SFU operations an element:
 // two exponentials, a reciprocal, an inverse root (f g = w rsqrt(w (1 + e^-x)^2),
 // w = 1 - a^2), two more with z; the decay's exponential is a polynomial
-// (decay2), which also gives 1 - a without cancellation.
+// (decay2), which also gives 1 - a without cancellation.  Where g is below some
+// 2^-64, w (1 + e^-x)^2 is infinite and the drive 0.
 template <typename T, bool ASYNC, bool GATE, bool START>
 __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kernel(const GatedParams p) {
   constexpr int STEPS = kGatedFwdSteps, VEC = gated_vec<T>(), E = STEPS * VEC, NT = GATE ? 4 : 3;
