@@ -514,7 +514,8 @@ ssm_status ss2d_cross_merge(const void *ys, void *y, int64_t b, int64_t H,
  * and h_last[i,d] = h after the last step.  A holds log decays, values <= 0
  * (above 0 the root has no value: NaN).
  * A decay is positive however small (below 2^-126 it is taken as that): a NaN
- * or an infinite state stays one until a sequence starts.
+ * or an infinite state stays one until a sequence starts.  An input gate g below
+ * some 2^-64 counts as 0 in the forward.
  *
  *   u, gate_a, gate_x, z, y   device rows (b L, d_in), dtype; z nullable
  *   A                         device fp32 (d_in)
@@ -545,8 +546,7 @@ size_t ssm_gated_scan_states_bytes(int64_t b, int64_t L, int64_t d_in);
  *     dl = lam (a h_{t-1} - a^2 g u / f)   (0 where a sequence starts, and its
  *                                           second term 0 where f = 0)
  *     dA = sum dl r;  dgate_a = dl A r (1 - r);  dh0 = a_0 lam_0
- * dbias_a, dbias_x are the sums of dgate_a, dgate_x over b and L.  Gates below
- * 2^-60 are taken as that.
+ * dbias_a, dbias_x are the sums of dgate_a, dgate_x over b and L.
  *
  *   dout                       device rows (b L, d_in), dtype
  *   dh_last                    device fp32 (b, d_in), nullable (0)

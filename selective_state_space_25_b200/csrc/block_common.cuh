@@ -23,15 +23,10 @@ constexpr float kDecayQ3 = 9.618237615e-03f;
 constexpr float kDecayQ4 = 1.339073526e-03f;
 constexpr float kDecayQ5 = 1.540351223e-04f;
 
-// max / min that keep a NaN operand.
+// max that keeps a NaN operand.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 __device__ __forceinline__ float rsqrt_approx(float x) {

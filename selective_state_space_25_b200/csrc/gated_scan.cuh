@@ -570,10 +570,8 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kern
 }
 
 // ---------------------------------------------------------------- backward
-// The same tiles from the last to the first.  Per element four SFU operations (r
-// and g share a reciprocal: 1 / ((1 + e^-ra)(1 + e^-gx)), exponentials capped at
-// 2^60 so that their product stays finite, which bounds the gates at 2^-60 from
-// below), two more with z.  a, f, a^2 / f, g and the adjoint stay in registers; r
+// The same tiles from the last to the first.  Per element five SFU operations, two
+// more with z.  a, f, a^2 / f, g and the adjoint stay in registers; r
 // is put back over the staged gates it came from.
 template <typename T, bool ASYNC, bool GATE, bool START>
 __global__ void __launch_bounds__(kGatedThreads, kGatedBwdCtas) gated_bwd_kernel(const GatedBwdParams q_) {
@@ -683,13 +681,9 @@ __global__ void __launch_bounds__(kGatedThreads, kGatedBwdCtas) gated_bwd_kernel
     float a[E], f[E], af[E], g[E], lam[E];  // af = a^2 / f; lam: dout silu(z), later the adjoint
 #pragma unroll
     for (int q = 0; q < E / 2; ++q) {
-      float2 er = ex2_2(fma2(staged_pair<T>(s + kRows, q, lane), f2(-kLog2e), k.na));
-      float2 eg = ex2_2(fma2(staged_pair<T>(s + 2 * kRows, q, lane), f2(-kLog2e), k.nx));
-      constexpr float kCap = 1152921504606846976.0f;  // 2^60
-      er = __fadd2_rn(make_float2(min_nan(er.x, kCap), min_nan(er.y, kCap)), f2(1.0f));
-      eg = __fadd2_rn(make_float2(min_nan(eg.x, kCap), min_nan(eg.y, kCap)), f2(1.0f));
-      const float2 inv = rcp_2(mul2(er, eg));
-      const float2 r = mul2(inv, eg), gv = mul2(inv, er);
+      const float2 er = ex2_2(fma2(staged_pair<T>(s + kRows, q, lane), f2(-kLog2e), k.na));
+      const float2 eg = ex2_2(fma2(staged_pair<T>(s + 2 * kRows, q, lane), f2(-kLog2e), k.nx));
+      const float2 r = rcp_2(__fadd2_rn(er, f2(1.0f))), gv = rcp_2(__fadd2_rn(eg, f2(1.0f)));
       float2 av, w;
       decay2(mul2(k.A2, r), av, w);
       float2 rho = rsqrt_2(w);

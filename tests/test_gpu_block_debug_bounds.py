@@ -22,7 +22,7 @@ def test_block_operators_stay_in_bounds_under_the_debug_build():
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-1000:]
 
 
-@pytest.mark.parametrize("name", ["random", "rounds", "eps", "ends", "nonfinite"])
+@pytest.mark.parametrize("name", ["random", "rounds", "eps", "ends", "nonfinite", "closed"])
 def test_more_block_operators_stay_in_bounds_under_the_debug_build(name):
     """The other sizes, too: seeded random ones, many rounds, odd row counts."""
     from selective_state_space_25_b200 import build as libbuild

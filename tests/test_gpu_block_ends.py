@@ -2,10 +2,7 @@
 and its decays 0 and 1, against automatic differentiation in 64 bits.
 
 Limit: 2^-14 of the largest value that the terms can reach, as in
-test_gpu_block.test_gated_scan_gates_at_their_ends.  The backward bounds a gate
-from below by 2^-60; where it is smaller, or 0, the part sqrt(r / (2 |A|)) of a
-step's dA (times lam g u, and A for dgate_a) is that of 2^-60 instead: below
-2^-20 for |A| >= 1e-6."""
+test_gpu_block.test_gated_scan_gates_at_their_ends."""
 import pytest
 import torch
 
