@@ -135,8 +135,9 @@ template <bool START> __device__ __forceinline__ float through(float P, float h,
 }
 // Product of two maps' decays; with START one of 0 stays 0 beside a NaN.
 template <bool START> __device__ __forceinline__ float times(float P, float a) {
+  if constexpr (!START) return P * a;  // held above 0 where its composition ends
   const float r = max_nan(P * a, kDecayMinP);
-  return START && (P == 0.0f || a == 0.0f) ? 0.0f : r;
+  return P == 0.0f || a == 0.0f ? 0.0f : r;
 }
 
 // States of VEC channels after the map m, (P, P, Q, Q).
@@ -184,6 +185,14 @@ template <int VEC, bool START> __device__ __forceinline__ void gated_compose(flo
   }
 }
 
+// Ends a composition: its P as other maps and states meet it.
+template <int VEC, bool START> __device__ __forceinline__ void gated_compose_end(float4 &m) {
+  if constexpr (!START) {
+    m.x = max_nan(m.x, kDecayMinP);
+    if constexpr (VEC == 2) m.y = max_nan(m.y, kDecayMinP);
+  }
+}
+
 // (P, P, Q, Q) of another lane.
 __device__ __forceinline__ float4 shfl4(float4 v, int lane) {
   return make_float4(__shfl_sync(~0u, v.x, lane), __shfl_sync(~0u, v.y, lane),
@@ -203,6 +212,7 @@ __device__ __forceinline__ void gated_parts(int S, int lane, float4 &own, float4
     own = shfl4(mine, lane ^ 16);
     all = own;
     gated_compose<VEC, START>(all, mine);
+    gated_compose_end<VEC, START>(all);
     return;
   }
   const int lc = 32 / S, part = lane / lc, l = lane % lc;
@@ -213,6 +223,8 @@ __device__ __forceinline__ void gated_parts(int S, int lane, float4 &own, float4
     if (s == part) own = all;
     gated_compose<VEC, START>(all, m);
   }
+  gated_compose_end<VEC, START>(own);
+  gated_compose_end<VEC, START>(all);
 }
 
 // Makes the tiles' compositions, which one warp of each CTA wrote, known to all
@@ -504,6 +516,7 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kern
       if (warp == kGatedWarps - 1) {
         float4 all = ahead;
         gated_compose<VEC, START>(all, wsum[par][warp][l]);
+        gated_compose_end<VEC, START>(all);
         for (int w = 0; w < C; ++w) st_peer(&csum[(par * C + rank) * 32 + lane], w, all);
       }
       gated_arrive(warp == kGatedWarps - 1);
@@ -515,6 +528,7 @@ __global__ void __launch_bounds__(kGatedThreads, gated_ctas<T>()) gated_fwd_kern
         }
         gated_apply<VEC, START>(h, csum[(par * C + w) * 32 + lane]);
       }
+      gated_compose_end<VEC, START>(ahead);
       gated_apply<VEC, START>(hs, ahead);
     }
     const int t_now = t_warp + it * tile_rows;
@@ -780,6 +794,7 @@ __global__ void __launch_bounds__(kGatedThreads, kGatedBwdCtas) gated_bwd_kernel
       if (warp == 0) {
         float4 all = behind;
         gated_compose<VEC, START>(all, wsum[par][warp][l]);
+        gated_compose_end<VEC, START>(all);
         for (int w = 0; w < C; ++w) st_peer(&csum[(par * C + rank) * 32 + lane], w, all);
       }
       gated_arrive(warp == 0);
@@ -791,6 +806,7 @@ __global__ void __launch_bounds__(kGatedThreads, kGatedBwdCtas) gated_bwd_kernel
         }
         gated_apply<VEC, START>(mu, csum[(par * C + w) * 32 + lane]);
       }
+      gated_compose_end<VEC, START>(behind);
       gated_apply<VEC, START>(mb, behind);
     }
     if (part < S - 1) gated_apply<VEC, START>(mb, back);
