@@ -23,11 +23,11 @@
 // the end, and recomputes the states from those that the forward kept (4 bytes
 // every 32 steps and channel).
 //
-// Measured (B200, b = 8, L = 2048, d = 1536, bf16, us): forward 58, backward 135
-// (floors 31 and 54 at the copy bandwidth); with z 70 and 165; fp32 79 and 147 (61,
+// Measured (B200, b = 8, L = 2048, d = 1536, bf16, us): forward 58, backward 130
+// (floors 31 and 54 at the copy bandwidth); with z 69 and 162; fp32 78 and 147 (61,
 // 108).  bf16 is bound by latency at 16 warps an SM and its part-filled second wave
-// (384 CTAs over 296 places): 39 and 100 instructions an element, issue slots 56-62 %
-// full, SFU 47 and 22 %.
+// (384 CTAs over 296 places): 39 and 97 instructions an element, issue slots 56-62 %
+// full, SFU 47 and 28 %.
 #pragma once
 
 #include <type_traits>
